@@ -451,7 +451,8 @@ cudaError_t launch_absorb_tc(const void* q_nope, const void* q_rope, const int* 
       !tmap_3d_batch(&tq, q_nope, (uint64_t)a.K, (uint64_t)a.H, (uint64_t)a.B, (uint32_t)a.Bp))
     return cudaErrorInvalidValue;
   const int operands = 2 * a.K * 128 + (a.K / 64) * a.Bp * 128;
-  const int smem = 1024 + (operands > a.Bp * 256 ? operands : a.Bp * 256);  // operands, later the output stage
+  const int stage = (a.Bp + 31) / 32 * 32 * 256;  // the epilogue stages 32 rows at a time
+  const int smem = 1024 + (operands > stage ? operands : stage);  // operands, later the output stage
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(absorb_tc_kernel), smem);
   if (e != cudaSuccess) return e;
   absorb_tc_kernel<<<dim3(a.H, a.d_c / 128), 128, smem, st>>>(tw, tq, (const __nv_bfloat16*)q_rope, q_pos,
