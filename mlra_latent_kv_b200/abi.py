@@ -1,8 +1,12 @@
-"""ctypes binding of libmlra (include/mlra.h): argument marshalling only.
+"""ctypes binding of libmlra (include/mlra.h, include/mlra_serving.h): argument
+marshalling only.
 
 Every computation runs in the CUDA library; this module turns torch tensors
 into device pointers and status codes into exceptions.  It fails loudly if the
 library is missing -- there is no other implementation behind these names.
+The calls of mlra_serving.h also check their tensors' shapes, types, layout
+and device here, and run on the tensors' device (its current stream, unless
+one is given).
 """
 from __future__ import annotations
 
@@ -42,11 +46,19 @@ def make_dims(*, B, H, d_h, d_v, d_c, d_r, max_pages_per_seq, num_pages, n_branc
                 KERNELS[kernel])
 
 
+class PromptShape(ctypes.Structure):
+    """Layout of mla_prompt's packed arrays: rows, kv heads and {token, head} strides in elements."""
+    _fields_ = [("kv_heads", ctypes.c_int), ("total_q", ctypes.c_int), ("total_k", ctypes.c_int),
+                ("q_nope_stride", ctypes.c_longlong * 2), ("q_rope_stride", ctypes.c_longlong * 2),
+                ("k_nope_stride", ctypes.c_longlong * 2), ("v_stride", ctypes.c_longlong * 2)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I32P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _DIMS = ctypes.POINTER(Dims)
+_SHAPE = ctypes.POINTER(PromptShape)
 _DECODE_ARGS = [_DIMS, _P, _P, _I32P, _P, _P, _P, _P, _I32P, _I32P, _P, _P, _SZ, _P]
 
 SIGNATURES = {
@@ -66,6 +78,13 @@ SIGNATURES = {
     "mlra_merge_upproj": (ctypes.c_int, [_DIMS, ctypes.c_int, _P, _P, _P, _P, _P, _SZ, _P]),
     "mlra_quantize_pages_fp8": (ctypes.c_int, [_DIMS, _P, _P, _P, _P, _P, _P, _P]),
     "mlra_decode_fp8": (ctypes.c_int, [_DIMS, _P, _P, _I32P, _P, _P, _P, _P, _P, _P, _I32P, _I32P, _P, _P, _SZ, _P]),
+    "mla_prompt_workspace_bytes": (_SZ, [_DIMS, _SHAPE]),
+    "mla_prompt": (ctypes.c_int, [_DIMS, _SHAPE, _P, _P, _I32P, _P, _P, _I32P, _P, _I32P, _P, _P, _P, _SZ, _P]),
+    "mlra_absorb": (ctypes.c_int, [_DIMS, _P, _P, _I32P, _P, _P, _P, _SZ, _P]),
+    "mlra_attention_weights": (ctypes.c_int, [_DIMS, _P, _P, _P, _P, _I32P, _I32P, _P, _P, _P, _SZ, _P]),
+    "latent_evict_workspace_bytes": (_SZ, [_DIMS]),
+    "latent_evict": (ctypes.c_int, [_DIMS, ctypes.c_int, _I32P, _P, _I32P, _I32P, _P, _P, _P, _I32P, _I32P, _P, _SZ,
+                                    _P]),
     "mlra_check_status": (ctypes.c_int, [_P, _P]),
     "mlra_selftest_wait_timeout": (ctypes.c_int, [_P, ctypes.c_longlong, _P]),
     "mlra_last_error": (ctypes.c_char_p, []),
@@ -245,6 +264,128 @@ def latent_append_noalloc(dims, d_model, h, W_DKV, W_KR, pos, page_table, latent
     _check(lib().latent_append_noalloc(ctypes.byref(dims), int(d_model), _ptr(h), _ptr(W_DKV), _ptr(W_KR),
                                        _ptr(pos), _ptr(page_table), _ptr(latent_cache), _ptr(rope_cache),
                                        _stream(stream)))
+
+
+class _Args:
+    """The tensors of one call: checked for shape, type, layout and a common
+    device before anything is enqueued, then passed on that device."""
+
+    def __init__(self, dims: Dims):
+        self.device = None
+        self.dtype = {v: k for k, v in DTYPES.items()}[dims.dtype]
+
+    def __call__(self, name, x, shape, dtype, strided=False):
+        import torch
+        want = {"f32": torch.float32, "bf16": torch.bfloat16, "i32": torch.int32, "bytes": torch.uint8}[dtype]
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise MlraError(1, f"{name} has to be a CUDA tensor")
+        if self.device is None:
+            self.device = x.device
+        if x.device != self.device:
+            raise MlraError(1, f"{name} is on {x.device}, others on {self.device}")
+        if x.dtype != want and dtype != "bytes":
+            raise MlraError(1, f"{name} is {x.dtype}, not {want}")
+        if shape is not None and tuple(x.shape) != tuple(shape):
+            raise MlraError(1, f"{name} has shape {tuple(x.shape)}, not {tuple(shape)}")
+        if not (x.stride(-1) == 1 or x.shape[-1] == 1 or x.numel() == 0) if strided else not x.is_contiguous():
+            raise MlraError(1, f"{name} has to be contiguous" + (" in its last axis" if strided else ""))
+        return x.data_ptr() or None
+
+    def workspace(self, x):
+        return self("workspace", x, None, "bytes"), x.numel() * x.element_size()
+
+    def run(self, fn, stream, *args):
+        import torch
+        with torch.cuda.device(self.device):
+            _check(fn(*args, _stream(stream)))
+
+
+def _prompt_shape(q_nope, q_rope, k_nope, v) -> PromptShape:
+    s = PromptShape(k_nope.shape[1], q_nope.shape[0], k_nope.shape[0])
+    for name, x in (("q_nope_stride", q_nope), ("q_rope_stride", q_rope), ("k_nope_stride", k_nope), ("v_stride", v)):
+        getattr(s, name)[:] = x.stride()[:2]
+    return s
+
+
+def prompt_workspace_bytes(dims: Dims, total_q: int, total_k: int, kv_heads: int) -> int:
+    """Bytes of workspace mla_prompt needs for that many packed rows and kv heads, whatever their strides."""
+    s = PromptShape(kv_heads, total_q, total_k)
+    for name, heads, width in (("q_nope_stride", dims.H, dims.d_h), ("q_rope_stride", dims.H, dims.d_r),
+                               ("k_nope_stride", kv_heads, dims.d_h), ("v_stride", kv_heads, dims.d_v)):
+        getattr(s, name)[:] = (heads * width, width)
+    n = lib().mla_prompt_workspace_bytes(ctypes.byref(dims), ctypes.byref(s))
+    if n == 0:
+        raise MlraError(1, last_error())
+    return int(n)
+
+
+def mla_prompt(dims, q_nope, q_rope, cu_q, k_nope, v, cu_k, rope_cache, page_table, out, workspace, lse=None,
+               stream=None):
+    """Causal attention of packed prompts into out [total_q,H,d_v] (see include/mlra_serving.h); q_nope, q_rope,
+    k_nope and v may be strided views, k_nope.shape[1] is the number of kv heads."""
+    d, a = dims, _Args(dims)
+    for name, x in (("q_nope", q_nope), ("k_nope", k_nope)):
+        if getattr(x, "ndim", 0) != 3:
+            raise MlraError(1, f"{name} has to be [tokens, heads, width]")
+    T, S, kv = q_nope.shape[0], k_nope.shape[0], k_nope.shape[1]
+    args = (a("q_nope", q_nope, (T, d.H, d.d_h), a.dtype, True), a("q_rope", q_rope, (T, d.H, d.d_r), a.dtype, True),
+            a("cu_q", cu_q, (d.B + 1,), "i32"), a("k_nope", k_nope, (S, kv, d.d_h), a.dtype, True),
+            a("v", v, (S, kv, d.d_v), a.dtype, True), a("cu_k", cu_k, (d.B + 1,), "i32"),
+            a("rope_cache", rope_cache, (d.num_pages, d.page_size, d.d_r), a.dtype),
+            a("page_table", page_table, (d.B, d.max_pages_per_seq), "i32"), a("out", out, (T, d.H, d.d_v), a.dtype),
+            None if lse is None else a("lse", lse, (T, d.H), "f32"), *a.workspace(workspace))
+    if T == 0:
+        return
+    shape = _prompt_shape(q_nope, q_rope, k_nope, v)
+    a.run(lib().mla_prompt, stream, ctypes.byref(dims), ctypes.byref(shape), *args)
+
+
+def absorb_query(dims, q_nope, q_rope, q_pos, W_UK, q_abs, workspace, stream=None):
+    """The decode's query folded through W_UK and rotated, times scale * log2(e), into q_abs [B,H,d_c+d_r]."""
+    d, a = dims, _Args(dims)
+    args = (a("q_nope", q_nope, (d.B, d.H, d.d_h), a.dtype), a("q_rope", q_rope, (d.B, d.H, d.d_r), a.dtype),
+            a("q_pos", q_pos, (d.B,), "i32"), a("W_UK", W_UK, (d.H, d.d_h, d.d_c), a.dtype),
+            a("q_abs", q_abs, (d.B, d.H, d.d_c + d.d_r), a.dtype), *a.workspace(workspace))
+    a.run(lib().mlra_absorb, stream, ctypes.byref(dims), *args)
+
+
+def _pools(a, d, latent_cache, rope_cache):
+    return (a("latent_cache", latent_cache, (d.num_pages, d.page_size, d.d_c), a.dtype),
+            a("rope_cache", rope_cache, (d.num_pages, d.page_size, d.d_r), a.dtype))
+
+
+def attention_weights(dims, q_abs, lse, latent_cache, rope_cache, page_table, seq_lens, weights_in, weights, workspace,
+                      stream=None):
+    """weights = weights_in (None: zeros) + each cached token's attention weight over all heads and branches."""
+    d, a = dims, _Args(dims)
+    slots = (d.B, d.max_pages_per_seq * d.page_size)
+    args = (a("q_abs", q_abs, (d.B, d.H, d.d_c + d.d_r), a.dtype), a("lse", lse, (d.B, d.n_branch, d.H), "f32"),
+            *_pools(a, d, latent_cache, rope_cache), a("page_table", page_table, (d.B, d.max_pages_per_seq), "i32"),
+            a("seq_lens", seq_lens, (d.B,), "i32"),
+            None if weights_in is None else a("weights_in", weights_in, slots, "f32"),
+            a("weights", weights, slots, "f32"), *a.workspace(workspace))
+    a.run(lib().mlra_attention_weights, stream, ctypes.byref(dims), *args)
+
+
+def evict_workspace_bytes(dims: Dims) -> int:
+    n = lib().latent_evict_workspace_bytes(ctypes.byref(dims))
+    if n == 0:
+        raise MlraError(1, last_error())
+    return int(n)
+
+
+def latent_evict(dims, recent, evict_pages, weights, page_table, seq_lens, latent_cache, rope_cache, weights_out,
+                 page_table_out, seq_lens_out, workspace, stream=None):
+    """Frees evict_pages[b] pages of each sequence: the tokens with the least weight leave, but for the last
+    ``recent`` (see include/mlra_serving.h)."""
+    d, a = dims, _Args(dims)
+    slots, table = (d.B, d.max_pages_per_seq * d.page_size), (d.B, d.max_pages_per_seq)
+    args = (a("evict_pages", evict_pages, (d.B,), "i32"), a("weights", weights, slots, "f32"),
+            a("page_table", page_table, table, "i32"), a("seq_lens", seq_lens, (d.B,), "i32"),
+            *_pools(a, d, latent_cache, rope_cache), a("weights_out", weights_out, slots, "f32"),
+            a("page_table_out", page_table_out, table, "i32"), a("seq_lens_out", seq_lens_out, (d.B,), "i32"),
+            *a.workspace(workspace))
+    a.run(lib().latent_evict, stream, ctypes.byref(dims), int(recent), *args)
 
 
 def check_status(workspace, stream=None) -> None:

@@ -38,7 +38,7 @@ def sources() -> list[str]:
 
 def _deps() -> list[str]:
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        [os.path.join(ROOT, "include", "mlra.h"), os.path.abspath(__file__)]
+        sorted(glob.glob(os.path.join(ROOT, "include", "*.h"))) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
