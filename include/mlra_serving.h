@@ -106,8 +106,9 @@ MLRA_SERVING_API mlra_status mla_prompt(const mlra_dims* dims, const mla_prompt_
  *     the same buffer as weights to add in place (no partial overlap)
  *   weights [B, max_pages_per_seq * page_size] fp32
  * The same inputs give the same bits.  workspace: at least 256 bytes, 256-byte
- * aligned.  Kernel AUTO runs the tcgen05 kernel for bf16, d_r = 64, H <= 128
- * and branches of a multiple of 64 dims, and the CUDA-core kernel otherwise.
+ * aligned.  Kernel AUTO runs the tcgen05 kernel for bf16, d_r = 64, branches
+ * of a multiple of 64 dims and n_branch * H (H rounded up to 32, at most 128)
+ * <= 512, and the CUDA-core kernel otherwise.
  * ------------------------------------------------------------------------- */
 MLRA_SERVING_API mlra_status mlra_absorb(const mlra_dims* dims, const void* q_nope, const void* q_rope,
                                          const int32_t* q_pos, const void* W_UK, void* q_abs, void* workspace,

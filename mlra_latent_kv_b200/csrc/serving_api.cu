@@ -244,13 +244,21 @@ mlra_status mlra_attention_weights(const mlra_dims* dims, const void* q_abs, con
       st = bad(MLRA_ERR_INVALID_ARG, "weights_in and weights overlap in part");
     if (st == MLRA_OK) st = check_workspace(workspace, workspace_bytes, kErrBytes);
     if (st != MLRA_OK) return st;
-    if (d->kernel == MLRA_KERNEL_TC)
-      return bad(MLRA_ERR_UNSUPPORTED, "the tcgen05 weights kernel needs bf16, d_r=64, H<=128, 64-dim branch blocks");
+    const bool tc_ok = weights_tc_supported(d->dtype, d->H, d->d_c, d->d_r, d->n_branch);
+    if (d->kernel == MLRA_KERNEL_TC && !tc_ok)
+      return bad(MLRA_ERR_UNSUPPORTED,
+                 "the tcgen05 weights kernel needs bf16, d_r=64, branches of a multiple of 64 dims, H<=128 and "
+                 "n_branch * H (in steps of 32) <= 512");
     const int sms = device_sms();
     if (sms == 0) return MLRA_ERR_CUDA;
     const WeightArgs a{d->B, d->H, d->d_c, d->d_r, d->n_branch, d->max_pages_per_seq, d->num_pages};
+    int* err = static_cast<int*>(workspace);
+    if (tc_ok && d->kernel != MLRA_KERNEL_SIMT)
+      return launched(launch_weights_tc(q_abs, lse, latent_cache, rope_cache, page_table, seq_lens, weights_in,
+                                        weights, err, a, sms, stream),
+                      "attention weights");
     return launched(launch_weights_simt(d->dtype, q_abs, lse, latent_cache, rope_cache, page_table, seq_lens,
-                                        weights_in, weights, static_cast<int*>(workspace), a, sms, stream),
+                                        weights_in, weights, err, a, sms, stream),
                     "attention weights");
   });
 }
