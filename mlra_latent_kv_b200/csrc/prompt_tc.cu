@@ -1,0 +1,682 @@
+// tcgen05 prompt attention: causal attention of packed prompts in the
+// unabsorbed form, 128 + 64 score dims and 128 value dims (sm_100a).
+//
+//   x[i,j] = scale * (q_nope_i . k_nope_j + RoPE(q_rope_i) . k_j),  j <= Lk - Lq + i
+//   out_i  = softmax_j(x) v                      (yololab.net, "超越 GQA 的推理
+//   革命…", sections "1. 鍵值聯合低秩壓縮" and "2. 解耦旋轉位置編碼")
+//
+// Bound by the tensor cores: 640 flops per (query, key, head); K and V of a
+// head come from L2 after the first query tile has fetched them.
+//
+// Design (B200):
+//   * Rows of a tile are (token, head of the kv group) pairs: with grouped
+//     heads as many heads as divide the group (a power of two) share a tile,
+//     so their keys are read once and a chunk of few tokens still fills the
+//     128 rows.  The rotary keys are shared by all heads and come from the
+//     paged cache, a page per copy.
+//   * A work item is two tiles (256 rows) of one sequence and head group,
+//     which share every K and V block; a persistent CTA per SM takes items
+//     from a counter, longest first within groups of heads whose K and V fit
+//     in L2 together.
+//   * TMEM: two score buffers (128 columns each; P, in bf16, overwrites the
+//     scores it came from) and two output accumulators, all 512 columns.
+//     While one tile's softmax runs, the tensor cores work on the other:
+//     PV and the next QK^T of tile A, then of tile B.
+//   * Shared memory: the two query tiles (96 KB) and a ring of eight 16 KB
+//     blocks (a key tile of 128 tokens is three of 64 dims, a value tile two of
+//     64 tokens), so that loads run more than a tile ahead.
+//   * Softmax: a thread per row, running maximum and sum in fp32, base 2.  The
+//     exponentials are taken against the maximum so far, in the same pass that
+//     finds the step's own, with P held back in registers; only when a row's
+//     maximum has grown by more than 2^8 the scores are read again and O, which
+//     the same thread owns, is rescaled: the scores of step j being there
+//     implies that PV of step j - 1 is done.
+//   * Value rows past a sequence's end are zeroed in shared memory before the
+//     product (a NaN there would get past P = 0); key rows past it are masked.
+//   * The rotation of the queries runs in the kernel before this one, beside
+//     the plan (sequences checked, items sorted by length); its output is
+//     bf16, as the tensor cores want it.
+//   * Every wait is bounded; a CTA that gives up records the site, lets its
+//     copies and MMAs in flight end and leaves.
+#include <cuda.h>
+
+#include "host_cache.h"
+#include "launch.h"
+#include "serving.h"
+#include "serving_ptx.cuh"
+
+namespace mlra {
+namespace {
+
+using namespace ptx;
+
+constexpr int kPtBlock = 128 * 128;  // 128 rows x 64 bf16, or 64 tokens x 128 bf16 as two halves
+constexpr int kPtRing = 8;
+constexpr int kPtThreads = 12 * 32;  // 0 loads, 1 MMAs, 2-3 idle, 4-7 softmax of tile A, 8-11 of tile B
+constexpr int kPtSmem = 6 * kPtBlock + kPtRing * kPtBlock;
+constexpr uint32_t kPtColO = 256;
+constexpr float kPtRescale = 8.f;    // log2
+constexpr int kPlanThreads = 512;
+constexpr int kPlanBins = 1024;
+
+struct PromptItem {
+  int live;          // 0: no more items
+  int head0, kvh;    // first head of the tile's heads, their kv head
+  int tok0;          // first token of tile A
+  int Lq, Lk, q0, k0, b;
+  int n[2];          // key tiles of tile A and B
+};
+
+struct PromptBars {
+  uint64_t full[kPtRing], empty[kPtRing];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t item_full[2], item_empty[2];
+  uint64_t drain;
+  PromptItem item[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+enum { kPsRing = 60, kPsItem, kPsItemFree, kPsQ, kPsQFree, kPsK, kPsV, kPsP, kPsOFree, kPsS, kPsO };
+
+// ---------------------------------------------------------------------------
+// Plan and query rotation.  Block 0 checks the sequences and lists the pairs
+// of tiles, longest first (a counting sort over the number of key tiles);
+// the other blocks rotate the queries, a token per warp: lane i forms the
+// angle of pair i, each eight lanes take a head.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int key_tiles(const PromptSeq& s, int tok0, int tokens) {
+  const int last = min(tok0 + tokens, s.Lq) - 1;  // the tile's last query
+  if (last < tok0) return 0;
+  return (max(0, s.Lk - s.Lq + last + 1) + 127) / 128;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    prompt_plan_kernel(const __nv_bfloat16* __restrict__ q_rope, const int* __restrict__ cu_q,
+                       const int* __restrict__ cu_k, __nv_bfloat16* __restrict__ q_rot, int2* __restrict__ list,
+                       int* __restrict__ counts, int* __restrict__ err, PromptArgs a, int pack, RopeTable tab) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int TT = 128 / pack;  // tokens of a tile
+  grid_dep_launch();
+  if (blockIdx.x == 0) {
+    __shared__ int bins[kPlanBins], s_most, s_warp[32];
+    for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) bins[i] = 0;
+    if (threadIdx.x == 0) s_most = 1;
+    __syncthreads();
+    for (int b = threadIdx.x; b < a.B; b += kPlanThreads) {
+      const PromptSeq s = prompt_seq(cu_q, cu_k, b, a, err);
+      if (s.Lq > 0) atomicMax(&s_most, (s.Lk + 127) / 128);
+    }
+    __syncthreads();
+    const int most = s_most;
+    // bin 0 holds the longest; an order within a bin is as good as another
+    auto bin = [&](const PromptSeq& s, int pair) {
+      const int n = max(key_tiles(s, 2 * pair * TT, TT), key_tiles(s, (2 * pair + 1) * TT, TT));
+      return kPlanBins - 1 - (int)((long long)n * (kPlanBins - 1) / most);
+    };
+    for (int b = warp; b < a.B; b += kPlanThreads / 32) {
+      const PromptSeq s = prompt_seq(cu_q, cu_k, b, a, nullptr);
+      for (int p = lane; 2 * p * TT < s.Lq; p += 32) atomicAdd(&bins[bin(s, p)], 1);
+    }
+    __syncthreads();
+    {  // exclusive prefix sums of the bins, two a thread
+      const int v0 = bins[2 * threadIdx.x], v1 = bins[2 * threadIdx.x + 1];
+      const int incl = warp_incl_scan(v0 + v1);
+      if (lane == 31) s_warp[warp] = incl;
+      __syncthreads();
+      int before = 0;
+      for (int i = 0; i < warp; ++i) before += s_warp[i];
+      bins[2 * threadIdx.x] = before + incl - v0 - v1;
+      bins[2 * threadIdx.x + 1] = before + incl - v1;
+      if (threadIdx.x == kPlanThreads - 1) {
+        counts[0] = before + incl;  // entries of the list
+        counts[1] = 0;              // the next item
+      }
+    }
+    __syncthreads();
+    for (int b = warp; b < a.B; b += kPlanThreads / 32) {
+      const PromptSeq s = prompt_seq(cu_q, cu_k, b, a, nullptr);
+      for (int p = lane; 2 * p * TT < s.Lq; p += 32) list[atomicAdd(&bins[bin(s, p)], 1)] = make_int2(b, p);
+    }
+    return;
+  }
+  const int warps = (gridDim.x - 1) * (kPlanThreads / 32);
+  for (int t = (blockIdx.x - 1) * (kPlanThreads / 32) + warp; t < a.total_q; t += warps) {
+    int lo = 0, hi = a.B - 1;  // the last sequence that starts at t or before
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (__ldg(cu_q + mid) <= t)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const PromptSeq s = prompt_seq(cu_q, cu_k, lo, a, nullptr);
+    if (t < s.q0 || t >= s.q0 + s.Lq) continue;
+    float sn, cs;
+    rope_sincos(tab, lane, s.Lk - s.Lq + t - s.q0, &sn, &cs);
+    const int c = lane & 7;  // this lane's 16 bytes of a head: pairs 4 c .. 4 c + 3
+    float sn4[4], cs4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sn4[i] = __shfl_sync(0xffffffffu, sn, 4 * c + i);
+      cs4[i] = __shfl_sync(0xffffffffu, cs, 4 * c + i);
+    }
+#pragma unroll 4
+    for (int h = lane >> 3; h < a.H; h += 4) {
+      uint4 x = __ldg(reinterpret_cast<const uint4*>(q_rope + (size_t)t * a.q_rope_s[0] + (size_t)h * a.q_rope_s[1]) + c);
+      uint32_t* w = &x.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xffff0000u);
+        w[i] = pack_bf16x2(x0 * cs4[i] - x1 * sn4[i], x0 * sn4[i] + x1 * cs4[i]);
+      }
+      reinterpret_cast<uint4*>(q_rot + ((size_t)t * a.H + h) * 64)[c] = x;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The attention.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kPtThreads, 1)
+    prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant__ CUtensorMap tm_qr,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_rope, const int* __restrict__ cu_q,
+                     const int* __restrict__ cu_k, const int* __restrict__ page_table, const int2* __restrict__ list,
+                     int* counts, __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int* __restrict__ err,
+                     PromptArgs a, int pack, int unit_group) {
+  constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, false, false);
+  constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);  // V read MN-major
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;                 // [tile][64-dim block]
+  uint8_t* sR = smem + 6 * kPtBlock;  // the ring
+  PromptBars* bars = reinterpret_cast<PromptBars*>(smem + kPtSmem);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int TT = 128 / pack;
+
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < kPtRing; ++k) {
+      mbar_init(smem_u32(&bars->full[k]), 1);
+      mbar_init(smem_u32(&bars->empty[k]), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_u32(&bars->q_full[x]), 1);
+      mbar_init(smem_u32(&bars->q_empty[x]), 1);
+      mbar_init(smem_u32(&bars->s_full[x]), 1);
+      mbar_init(smem_u32(&bars->p_full[x]), 4);
+      mbar_init(smem_u32(&bars->o_full[x]), 1);
+      mbar_init(smem_u32(&bars->o_free[x]), 4);
+      mbar_init(smem_u32(&bars->item_full[x]), 1);
+      mbar_init(smem_u32(&bars->item_empty[x]), 9);  // the MMA warp and eight softmax warps
+    }
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&bars->tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  // the item of turn i, for a consumer; false when the CTA has given up
+  auto take = [&](uint32_t i, PromptItem* it) {
+    const int s = i & 1;
+    if (!mbar_wait_warp(smem_u32(&bars->item_full[s]), (i >> 1) & 1, abort_flag, err, kPsItem)) return false;
+    *it = bars->item[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[s]));
+    return true;
+  };
+
+  if (warp == 0) {
+    // --------------------------------------------------------------- loads
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_qn);
+      tma_prefetch_desc(&tm_qr);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      tma_prefetch_desc(&tm_rope);
+    }
+    grid_dep_wait();  // the plan and the rotated queries
+    const int nlist = *reinterpret_cast<volatile int*>(counts);
+    const int units = a.H / pack;
+    const long long total = (long long)nlist * units;
+    const long long group = (long long)nlist * unit_group;
+    uint32_t use = 0, tiles[2] = {0, 0};  // ring blocks and query tiles loaded so far
+    bool ok = true;
+    int w = 0;
+    if (lane == 0) w = atomicAdd(counts + 1, 1);
+    w = __shfl_sync(0xffffffffu, w, 0);
+    for (uint32_t i = 0; ok; ++i) {
+      int w_next = 0;
+      if (lane == 0 && w < total) w_next = atomicAdd(counts + 1, 1);  // not needed before the next turn
+      PromptItem it;
+      it.live = w < total;
+      if (it.live) {
+        const int g = (int)(w / group), r = (int)(w - g * group);
+        const int nu = min(unit_group, units - g * unit_group);  // units of this group
+        const int2 e = __ldcg(list + r / nu);
+        const int unit = g * unit_group + r % nu;
+        const PromptSeq s = prompt_seq(cu_q, cu_k, e.x, a, nullptr);
+        it.b = e.x;
+        it.head0 = unit * pack;
+        it.kvh = it.head0 / (a.H / a.kv_heads);
+        it.tok0 = 2 * e.y * TT;
+        it.Lq = s.Lq;
+        it.Lk = s.Lk;
+        it.q0 = s.q0;
+        it.k0 = s.k0;
+        it.n[0] = key_tiles(s, it.tok0, TT);
+        it.n[1] = key_tiles(s, it.tok0 + TT, TT);
+      }
+      const int sl = i & 1;
+      if (i >= 2 && !mbar_wait_warp(smem_u32(&bars->item_empty[sl]), ((i >> 1) - 1) & 1, abort_flag, err, kPsItemFree))
+        break;
+      if (lane == 0) {
+        bars->item[sl] = it;
+        mbar_arrive(smem_u32(&bars->item_full[sl]));
+      }
+      __syncwarp();
+      if (!it.live) break;
+      const int n = max(it.n[0], it.n[1]), np = npages_of(it.Lk);
+      // lane 0, 1: the ids of a key tile's pages, read a tile ahead
+      auto page_id = [&](int j) {
+        return lane < 2 && 2 * j + lane < np ? __ldg(page_table + (size_t)it.b * a.maxp + 2 * j + lane) : 0;
+      };
+      auto acquire = [&](uint32_t bytes) {  // the next ring block
+        const uint32_t k = use % kPtRing;
+        if (use >= (uint32_t)kPtRing)
+          ok = mbar_wait_warp(smem_u32(&bars->empty[k]), (use / kPtRing - 1) & 1, abort_flag, err, kPsRing);
+        if (ok && lane == 0) mbar_expect_tx(smem_u32(&bars->full[k]), bytes);
+        __syncwarp();
+        return k;
+      };
+      int id = page_id(0);
+      for (int j = 0; ok && j < n; ++j) {
+        const int id_next = j + 1 < n ? page_id(j + 1) : 0;
+        const int pages = min(2, np - 2 * j);
+        for (int blk = 0; ok && blk < 3; ++blk) {
+          const uint32_t k = acquire(blk < 2 ? kPtBlock : pages * (kPtBlock / 2));
+          if (!ok) break;
+          const uint32_t dst = smem_u32(sR + k * kPtBlock), fb = smem_u32(&bars->full[k]);
+          if (blk < 2) {
+            if (lane == 0) tma_load_3d(dst, &tm_k, fb, 64 * blk, it.kvh, it.k0 + 128 * j);
+          } else if (lane < pages) {
+            if (id < 0 || id >= a.num_pages) {  // reported, and read from page 0 instead
+              report_error(err, kErrDeviceCheck, it.b, (2 * j + lane) * kPage);
+              id = 0;
+            }
+            tma_load_2d(dst + lane * (kPtBlock / 2), &tm_rope, fb, 0, id * kPage);
+          }
+          __syncwarp();
+          ++use;
+        }
+        if (j == 0) {  // the query tiles, once the last QK^T of the item before has read theirs
+          for (int x = 0; ok && x < 2; ++x) {
+            if (it.n[x] == 0) continue;
+            if (tiles[x] > 0)
+              ok = mbar_wait_warp(smem_u32(&bars->q_empty[x]), (tiles[x] - 1) & 1, abort_flag, err, kPsQFree);
+            if (!ok) break;
+            if (lane == 0) {
+              const uint32_t fb = smem_u32(&bars->q_full[x]), dst = smem_u32(sQ + 3 * x * kPtBlock);
+              const int t = it.q0 + it.tok0 + x * TT;
+              mbar_expect_tx(fb, 3 * kPtBlock);
+              tma_load_3d(dst, &tm_qn, fb, 0, it.head0, t);
+              tma_load_3d(dst + kPtBlock, &tm_qn, fb, 64, it.head0, t);
+              tma_load_3d(dst + 2 * kPtBlock, &tm_qr, fb, 0, it.head0, t);
+            }
+            __syncwarp();
+            ++tiles[x];
+          }
+        }
+        for (int half = 0; ok && half < 2; ++half) {  // 64 tokens of V
+          const uint32_t k = acquire(kPtBlock);
+          if (!ok) break;
+          if (lane < 2)
+            tma_load_3d(smem_u32(sR + k * kPtBlock + lane * (kPtBlock / 2)), &tm_v, smem_u32(&bars->full[k]), 64 * lane,
+                        it.kvh, it.k0 + 128 * j + 64 * half);
+          __syncwarp();
+          ++use;
+        }
+        id = id_next;
+      }
+      w = __shfl_sync(0xffffffffu, w_next, 0);
+    }
+    if (*abort_flag) {
+      for (uint32_t u = use > (uint32_t)kPtRing ? use - kPtRing : 0; u < use; ++u)
+        drain_wait(smem_u32(&bars->full[u % kPtRing]), (u / kPtRing) & 1);
+      for (int x = 0; x < 2; ++x)
+        if (tiles[x] > 0) drain_wait(smem_u32(&bars->q_full[x]), (tiles[x] - 1) & 1);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
+    uint32_t base = 0;                                    // ring position of the item's first block
+    uint32_t tiles[2] = {0, 0}, steps[2] = {0, 0};        // query tiles begun, P buffers taken
+    bool ok = true;
+    PromptItem it;
+    for (uint32_t i = 0; ok && take(i, &it) && it.live; ++i) {
+      const int n = max(it.n[0], it.n[1]);
+      auto qk = [&](int x, int j) {
+        const uint32_t kp = base + 5u * j;
+        for (int blk = 0; blk < 3; ++blk) {
+          const uint32_t k = (kp + blk) % kPtRing;
+          ok = ok && mbar_wait_warp(smem_u32(&bars->full[k]), ((kp + blk) / kPtRing) & 1, abort_flag, err, kPsK);
+          if (!ok) return;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t qd = sdesc_sw128(smem_u32(sQ + (3 * x + blk) * kPtBlock), 16, 1024);
+            const uint64_t kd = sdesc_sw128(smem_u32(sR + k * kPtBlock), 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss(tmem + 128u * x, qd + (uint64_t)(2 * ks), kd + (uint64_t)(2 * ks), kIdescQK, (blk | ks) ? 1u : 0u);
+          }
+          __syncwarp();
+        }
+        if (lane == 0) {
+          mma_commit(smem_u32(&bars->s_full[x]));
+          if (x == 1 || j >= it.n[1])  // the last reader of these blocks
+            for (int blk = 0; blk < 3; ++blk) mma_commit(smem_u32(&bars->empty[(kp + blk) % kPtRing]));
+          if (j + 1 == it.n[x]) mma_commit(smem_u32(&bars->q_empty[x]));
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int x, int j) {
+        const uint32_t vp = base + 5u * j + 3u;
+        ok = ok && mbar_wait_warp(smem_u32(&bars->p_full[x]), steps[x] & 1, abort_flag, err, kPsP);
+        // the item before has read its O
+        if (ok && j == 0 && tiles[x] > 1)
+          ok = mbar_wait_warp(smem_u32(&bars->o_free[x]), (tiles[x] - 2) & 1, abort_flag, err, kPsOFree);
+        if (!ok) return;
+        ++steps[x];
+        const int rows = it.Lk - 128 * j;               // value rows inside the sequence
+        const bool first = x == 0 || j >= it.n[0];      // the first reader of these blocks
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t k = (vp + half) % kPtRing;
+          ok = mbar_wait_warp(smem_u32(&bars->full[k]), ((vp + half) / kPtRing) & 1, abort_flag, err, kPsV);
+          if (!ok) return;
+          uint8_t* blk = sR + k * kPtBlock;
+          const int have = rows - 64 * half;
+          if (first && have < 64) {
+            const int r0 = max(0, have), nz = (64 - r0) * 8;
+            for (int e = lane; e < 2 * nz; e += 32)
+              *reinterpret_cast<uint4*>(blk + (e / nz) * (kPtBlock / 2) + r0 * 128 + (e % nz) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t vd = sdesc_sw128(smem_u32(blk), kPtBlock / 2, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ts(tmem + kPtColO + 128u * x, tmem + 128u * x + 32u * half + 8u * ks,
+                     vd + (uint64_t)((ks * 2048) >> 4), kIdescPV, (j | half | ks) ? 1u : 0u);
+          }
+          __syncwarp();
+        }
+        if (lane == 0) {
+          if (x == 1 || j >= it.n[1]) {
+            mma_commit(smem_u32(&bars->empty[vp % kPtRing]));
+            mma_commit(smem_u32(&bars->empty[(vp + 1) % kPtRing]));
+          }
+          if (j + 1 == it.n[x]) mma_commit(smem_u32(&bars->o_full[x]));
+        }
+        __syncwarp();
+      };
+      for (int x = 0; ok && x < 2; ++x) {
+        if (it.n[x] == 0) continue;
+        ok = mbar_wait_warp(smem_u32(&bars->q_full[x]), tiles[x] & 1, abort_flag, err, kPsQ);
+        ++tiles[x];
+        if (ok) qk(x, 0);
+      }
+      for (int j = 0; ok && j < n; ++j)
+        for (int x = 0; ok && x < 2; ++x) {
+          if (j >= it.n[x]) continue;
+          pv(x, j);
+          if (ok && j + 1 < it.n[x]) qk(x, j + 1);
+        }
+      base += 5u * n;
+    }
+    if (*abort_flag) {
+      if (lane == 0) {
+        mma_commit(smem_u32(&bars->drain));
+        drain_wait(smem_u32(&bars->drain), 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------- softmax
+    const int x = (warp - 4) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_col = tmem + lane_off + 128u * x, o_col = tmem + lane_off + kPtColO + 128u * x;
+    const float sc = a.scale_log2, jump = kPtRescale / sc;
+    uint32_t steps = 0, tiles = 0;
+    bool ok = true;
+    PromptItem it;
+    for (uint32_t i = 0; ok && take(i, &it) && it.live; ++i) {
+      const int tok = it.tok0 + x * TT + row / pack, head = it.head0 + row % pack;
+      const bool mine = tok < it.Lq;
+      const int n = it.n[x];
+      const int lim = min(it.Lk - it.Lq + tok, it.Lk - 1);  // the row's last key
+      const size_t at = (size_t)(it.q0 + tok) * a.H + head;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++steps) {
+        ok = mbar_wait_warp(smem_u32(&bars->s_full[x]), steps & 1, abort_flag, err, kPsS);
+        if (!ok) break;
+        tc_fence_after();
+        const int cmax = lim - 128 * j;
+        const bool masked = __any_sync(0xffffffffu, cmax < 127);
+        // scores c0 .. c0 + 63 of the row, -inf past its last key
+        auto load = [&](int c0, uint32_t (&v)[32], uint32_t (&w)[32]) {
+          tmem_ld32x2(s_col + c0, s_col + c0 + 32, v, w);
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              if (c0 + c > cmax) v[c] = 0xff800000u;
+              if (c0 + 32 + c > cmax) w[c] = 0xff800000u;
+            }
+          }
+        };
+        auto largest = [&](float t, const uint32_t (&v)[32]) {
+          float t0 = t, t1 = __uint_as_float(v[0]);
+#pragma unroll
+          for (int c = 1; c < 31; c += 3) {
+            t0 = fmaxf(fmaxf(t0, __uint_as_float(v[c])), __uint_as_float(v[c + 1]));
+            t1 = fmaxf(t1, __uint_as_float(v[c + 2]));
+          }
+          return fmaxf(fmaxf(t0, t1), __uint_as_float(v[31]));
+        };
+        uint32_t p[4][16];  // P of 32 keys each, packed
+        float top, sum;
+        auto exponentials = [&] {
+          const float ref = m == -INFINITY ? 0.f : -m * sc;  // no key so far: every term is 2^-inf = 0
+          const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(ref, ref);
+          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          top = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[2][32];
+            load(64 * h, v[0], v[1]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              top = largest(top, v[g]);
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                float2 e = fma_f32x2(make_float2(__uint_as_float(v[g][2 * u]), __uint_as_float(v[g][2 * u + 1])), sc2,
+                                     ref2);
+                e.x = ex2(e.x);
+                e.y = ex2(e.y);
+                s2[u & 1] = add_f32x2(s2[u & 1], e);
+                p[2 * h + g][u] = pack_bf16x2(e.x, e.y);
+              }
+            }
+          }
+          sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+        };
+        if (j == 0) {
+          m = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[32], w[32];
+            load(64 * h, v, w);
+            m = largest(largest(m, v), w);
+          }
+        }
+        // against the maximum so far; the scores stay where they are until it is known that this will do
+        exponentials();
+        if (j > 0 && __any_sync(0xffffffffu, top > m + jump)) {
+          float corr = 1.f;
+          if (top > m + jump) {
+            corr = ex2((m - top) * sc);
+            m = top;
+          }
+          l *= corr;
+          exponentials();
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_col + c, o);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * corr);
+            tmem_st16(o_col + c, o);
+          }
+        }
+        l += sum;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) tmem_st16_async(s_col + 16u * g, p[g]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[x]));
+      }
+      if (!ok) break;
+      if (n > 0) {
+        ok = mbar_wait_warp(smem_u32(&bars->o_full[x]), tiles & 1, abort_flag, err, kPsO);
+        ++tiles;
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      __nv_bfloat16* dst = out + at * 128;
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        if (n > 0) tmem_ld32(o_col + c, o);
+        if (mine) {
+#pragma unroll
+          for (int u = 0; u < 32; u += 8) {
+            uint4 pk = make_uint4(0, 0, 0, 0);
+            if (l != 0.f) {
+              pk.x = pack_bf16x2(__uint_as_float(o[u]) * inv, __uint_as_float(o[u + 1]) * inv);
+              pk.y = pack_bf16x2(__uint_as_float(o[u + 2]) * inv, __uint_as_float(o[u + 3]) * inv);
+              pk.z = pack_bf16x2(__uint_as_float(o[u + 4]) * inv, __uint_as_float(o[u + 5]) * inv);
+              pk.w = pack_bf16x2(__uint_as_float(o[u + 6]) * inv, __uint_as_float(o[u + 7]) * inv);
+            }
+            *reinterpret_cast<uint4*>(dst + c + u) = pk;
+          }
+        }
+      }
+      if (n > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->o_free[x]));
+      }
+      if (lse && mine) lse[at] = l == 0.f ? -INFINITY : m * sc + log2f(l);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Heads of a kv group that share a tile: the largest power of two that divides the group, at most 128.
+int heads_packed(int H, int kv_heads) {
+  const int g = H / kv_heads, p = g & -g;
+  return p < 128 ? p : 128;
+}
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+long long list_entries(const PromptArgs& a, int pack) { return ((long long)a.total_q * pack + 255) / 256 + a.B; }
+
+}  // namespace
+
+bool prompt_tc_supported(int dtype, int d_h, int d_r, int d_v) {
+  return dtype == MLRA_BF16 && d_h == 128 && d_r == 64 && d_v == 128;
+}
+
+// error record | item counts | list of tile pairs | rotated queries
+size_t prompt_tc_workspace(const PromptArgs& a) {
+  const size_t list = round_up((size_t)list_entries(a, heads_packed(a.H, a.kv_heads)) * sizeof(int2), 256);
+  return 512 + list + round_up((size_t)a.total_q * a.H * 64 * 2, 256);
+}
+
+cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* cu_q, const void* k_nope,
+                             const void* v, const int* cu_k, const void* rope_cache, const int* page_table, void* out,
+                             float* lse, void* workspace, const PromptArgs& a, const RopeTable& tab, int sms,
+                             cudaStream_t st) {
+  const int pack = heads_packed(a.H, a.kv_heads), units = a.H / pack;
+  char* ws = static_cast<char*>(workspace);
+  int* err = reinterpret_cast<int*>(ws);
+  int* counts = reinterpret_cast<int*>(ws + 256);
+  int2* list = reinterpret_cast<int2*>(ws + 512);
+  const long long entries = list_entries(a, pack);
+  __nv_bfloat16* q_rot = reinterpret_cast<__nv_bfloat16*>(ws + 512 + round_up((size_t)entries * sizeof(int2), 256));
+
+  // packed [tokens][heads][width]; an axis of one element takes any valid stride
+  auto packed = [&](CUtensorMap* m, const void* p, int width, int heads, int rows, const long long* s, int box_heads,
+                    int box_rows) {
+    const uint64_t d[3] = {(uint64_t)width, (uint64_t)heads, (uint64_t)(rows > 0 ? rows : 1)};
+    const uint64_t by[2] = {(uint64_t)(heads > 1 && rows > 0 ? s[1] : width) * 2,
+                            (uint64_t)(rows > 1 ? s[0] : width) * 2};
+    const uint32_t box[3] = {64, (uint32_t)box_heads, (uint32_t)box_rows};
+    return encode_bf16_map(m, 3, p, d, by, box);
+  };
+  const long long rot_s[2] = {(long long)a.H * 64, 64};
+  CUtensorMap tqn, tqr, tk, tv, tr;
+  if (a.total_k == 0) k_nope = v = q_nope;  // no key to load: any address will do
+  const uint64_t rd[2] = {64, (uint64_t)a.num_pages * kPage}, rs[1] = {128};
+  const uint32_t rbox[2] = {64, 64};
+  if (!packed(&tqn, q_nope, 128, a.H, a.total_q, a.q_nope_s, pack, 128 / pack) ||
+      !packed(&tqr, q_rot, 64, a.H, a.total_q, rot_s, pack, 128 / pack) ||
+      !packed(&tk, k_nope, 128, a.kv_heads, a.total_k, a.k_nope_s, 1, 128) ||
+      !packed(&tv, v, 128, a.kv_heads, a.total_k, a.v_s, 1, 64) ||
+      !encode_bf16_map(&tr, 2, rope_cache, rd, rs, rbox))
+    return cudaErrorInvalidValue;
+
+  const int rot_blocks = (int)(((long long)a.total_q + kPlanThreads / 32 - 1) / (kPlanThreads / 32));
+  prompt_plan_kernel<<<1 + (rot_blocks < 8 * sms ? rot_blocks : 8 * sms), kPlanThreads, 0, st>>>(
+      static_cast<const __nv_bfloat16*>(q_rope), cu_q, cu_k, q_rot, list, counts, err, a, pack, tab);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  // units of heads whose K and V (256 values a token and kv head) take about 48 MB of L2 together
+  const long long bytes = (long long)a.total_k * 512 * a.kv_heads / units;
+  long long group = bytes > 0 ? (48LL << 20) / bytes : units;
+  group = group < 1 ? 1 : (group > units ? units : group);
+  const int smem = 1024 + kPtSmem + (int)sizeof(PromptBars);
+  e = ensure_smem(reinterpret_cast<const void*>(prompt_tc_kernel), smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(entries * units < sms ? entries * units : sms));
+  cfg.blockDim = dim3(kPtThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_tc_kernel, tqn, tqr, tk, tv, tr, cu_q, cu_k, page_table,
+                            static_cast<const int2*>(list), counts, static_cast<__nv_bfloat16*>(out), lse, err, a, pack,
+                            (int)group);
+}
+
+}  // namespace mlra

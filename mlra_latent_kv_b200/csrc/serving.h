@@ -65,6 +65,12 @@ __device__ __forceinline__ PromptSeq prompt_seq(const int* cu_q, const int* cu_k
   return PromptSeq{q0, k0, q1 - q0, k1 - k0};
 }
 
+bool prompt_tc_supported(int dtype, int d_h, int d_r, int d_v);
+size_t prompt_tc_workspace(const PromptArgs& a);
+cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* cu_q, const void* k_nope,
+                             const void* v, const int* cu_k, const void* rope_cache, const int* page_table, void* out,
+                             float* lse, void* workspace, const PromptArgs& a, const RopeTable& tab, int sms,
+                             cudaStream_t st);
 cudaError_t launch_prompt_simt(int dtype, const void* q_nope, const void* q_rope, const int* cu_q, const void* k_nope,
                                const void* v, const int* cu_k, const void* rope_cache, const int* page_table,
                                void* out, float* lse, int* err, const PromptArgs& a, const RopeTable& tab,

@@ -139,6 +139,36 @@ mlra_status check_prompt(const mlra_dims* d, const mla_prompt_shape* s) {
   return MLRA_OK;
 }
 
+PromptArgs prompt_args(const mlra_dims* d, const mla_prompt_shape* s) {
+  PromptArgs a{d->B,       d->H,       s->kv_heads, d->d_h, d->d_r, d->d_v, d->max_pages_per_seq, d->num_pages,
+               s->total_q, s->total_k, scale_log2(d), {}, {}, {}, {}};
+  for (int i = 0; i < 2; ++i) {
+    a.q_nope_s[i] = s->q_nope_stride[i];
+    a.q_rope_s[i] = s->q_rope_stride[i];
+    a.k_nope_s[i] = s->k_nope_stride[i];
+    a.v_s[i] = s->v_stride[i];
+  }
+  return a;
+}
+
+// The workspace does not depend on the strides: the tcgen05 kernel's where the widths are its own.
+size_t prompt_workspace(const mlra_dims* d, const PromptArgs& a) {
+  return d->kernel != MLRA_KERNEL_SIMT && prompt_tc_supported(d->dtype, d->d_h, d->d_r, d->d_v) ? prompt_tc_workspace(a)
+                                                                                                 : kErrBytes;
+}
+
+// Copies by the tensor memory accelerator: 16-byte addresses and strides.
+bool prompt_aligned(const PromptArgs& a, const void* q_nope, const void* q_rope, const void* k_nope, const void* v) {
+  const void* p[] = {q_nope, q_rope, k_nope, v};
+  const long long* s[] = {a.q_nope_s, a.q_rope_s, a.k_nope_s, a.v_s};
+  const int rows[] = {a.total_q, a.total_q, a.total_k, a.total_k}, heads[] = {a.H, a.H, a.kv_heads, a.kv_heads};
+  for (int i = 0; i < 4; ++i) {
+    if (rows[i] == 0) continue;
+    if (!aligned(p[i], 16) || (rows[i] > 1 && s[i][0] % 8) || (heads[i] > 1 && s[i][1] % 8)) return false;
+  }
+  return true;
+}
+
 }  // namespace
 }  // namespace mlra
 
@@ -150,7 +180,7 @@ size_t mla_prompt_workspace_bytes(const mlra_dims* dims, const mla_prompt_shape*
   size_t n = 0;
   guarded([&] {
     mlra_status st = check_prompt(dims, shape);
-    if (st == MLRA_OK) n = kErrBytes;
+    if (st == MLRA_OK) n = prompt_workspace(dims, prompt_args(dims, shape));
     return st;
   });
   return n;
@@ -172,21 +202,25 @@ mlra_status mla_prompt(const mlra_dims* dims, const mla_prompt_shape* shape, con
     if (s->total_q == 0) return MLRA_OK;  // nothing to write
     st = check_ptrs(ptrs, s->total_k == 0 ? 7 : 9);
     if (st == MLRA_OK && lse && !aligned(lse, 4)) st = bad(MLRA_ERR_INVALID_ARG, "lse is not 4-byte aligned");
-    if (st == MLRA_OK) st = check_workspace(workspace, workspace_bytes, kErrBytes);
+    const PromptArgs a = prompt_args(d, s);
+    if (st == MLRA_OK) st = check_workspace(workspace, workspace_bytes, prompt_workspace(d, a));
     if (st != MLRA_OK) return st;
-    if (d->kernel == MLRA_KERNEL_TC)
-      return bad(MLRA_ERR_UNSUPPORTED, "the tcgen05 prompt kernel needs bf16, d_h=128, d_r=64, d_v=128");
-    PromptArgs a{d->B,   d->H, s->kv_heads, d->d_h, d->d_r, d->d_v, d->max_pages_per_seq, d->num_pages, s->total_q,
-                 s->total_k, scale_log2(d), {}, {}, {}, {}};
-    for (int i = 0; i < 2; ++i) {
-      a.q_nope_s[i] = s->q_nope_stride[i];
-      a.q_rope_s[i] = s->q_rope_stride[i];
-      a.k_nope_s[i] = s->k_nope_stride[i];
-      a.v_s[i] = s->v_stride[i];
+    const bool tc_ok = prompt_tc_supported(d->dtype, d->d_h, d->d_r, d->d_v) &&
+                       prompt_aligned(a, q_nope, q_rope, k_nope, v);
+    if (d->kernel == MLRA_KERNEL_TC && !tc_ok)
+      return bad(MLRA_ERR_UNSUPPORTED,
+                 "the tcgen05 prompt kernel needs bf16, d_h=128, d_r=64, d_v=128 and 16-byte aligned rows");
+    const RopeTable tab = internal_rope_table(d);
+    if (tc_ok && d->kernel != MLRA_KERNEL_SIMT) {
+      const int sms = device_sms();
+      if (sms == 0) return MLRA_ERR_CUDA;
+      return launched(launch_prompt_tc(q_nope, q_rope, cu_q, k_nope, v, cu_k, rope_cache, page_table, out, lse,
+                                       workspace, a, tab, sms, stream),
+                      "prompt attention");
     }
     int* err = static_cast<int*>(workspace);
     return launched(launch_prompt_simt(d->dtype, q_nope, q_rope, cu_q, k_nope, v, cu_k, rope_cache, page_table, out,
-                                       lse, err, a, internal_rope_table(d), stream),
+                                       lse, err, a, tab, stream),
                     "prompt attention");
   });
 }

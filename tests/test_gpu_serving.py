@@ -162,6 +162,17 @@ def test_prompt_strides(interleaved, offset):
     p.check()
 
 
+def test_prompt_heads_first_layout():
+    """Tokens inside heads: a head's stride is larger than a token's."""
+    p = Prompt("bf16", (40, 200), (140, 200), 4, 2, interleaved=False, seed=3)
+    for name in ("q_nope", "q_rope", "k_nope", "v"):
+        x = getattr(p, name)
+        setattr(p, name, x.transpose(0, 1).contiguous().transpose(0, 1))
+    assert p.k_nope.stride(1) > p.k_nope.stride(0)
+    p.call()
+    p.check()
+
+
 def test_prompt_rising_scores():
     """Each key's score far above all before it: the running maximum moves in every step."""
     p = Prompt("bf16", (600,), (600,), 2, 2, seed=4)
