@@ -63,6 +63,18 @@ struct WtBars {
 
 static_assert(offsetof(WtBars, lse) % 16 == 0 && sizeof(WtBars) % 16 == 0, "16-byte reads");
 
+// A position in a ring of `n` barriers and the parity of its current round.
+struct RingPos {
+  int i = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void step(int n) {
+    if (++i == n) {
+      i = 0;
+      round ^= 1u;
+    }
+  }
+};
+
 enum { kWsRing = 40, kWsFull, kWsQEmpty, kWsQFull, kWsFree, kWsScores };
 
 // The tiles of CTA c of G, one after another.
@@ -162,7 +174,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ the cache
-    uint32_t use = 0;  // ring blocks filled so far
+    RingPos ring;
+    int filled = 0;  // blocks in the ring, up to its size
     bool ok = true;
     // lane j < 2: the id of page j of the tile, read a tile ahead
     auto page_id = [&](const TileCursor& c) {
@@ -180,12 +193,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         report_error(err, kErrDeviceCheck, cur.b, (2 * cur.t + lane) * kPage);
         id = 0;
       }
-      for (int k = 0; k < nblk; ++k, ++use) {
-        const uint32_t s = use % stages;
-        if (use >= (uint32_t)stages &&
-            !mbar_wait_warp(smem_u32(&bars->empty[s]), (use / stages - 1) & 1, abort_flag, err, kWsRing)) {
-          ok = false;
-          break;
+      for (int k = 0; k < nblk; ++k) {
+        const int s = ring.i;
+        if (filled == stages) {
+          ok = mbar_wait_warp(smem_u32(&bars->empty[s]), ring.round ^ 1u, abort_flag, err, kWsRing);
+          if (!ok) break;
+        } else {
+          ++filled;
         }
         const uint32_t fb = smem_u32(&bars->full[s]);
         if (lane == 0) mbar_expect_tx(fb, (uint32_t)np * (kWtBlock / 2));
@@ -194,13 +208,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           tma_load_2d(smem_u32(sT + s * kWtBlock + lane * (kWtBlock / 2)), k == 0 ? &tm_rope : &tm_lat, fb,
                       k == 0 ? 0 : 64 * (k - 1), id * kPage);
         __syncwarp();
+        ring.step(stages);
       }
       cur = next;
       id = id_next;
     }
-    if (!ok)
-      for (uint32_t u = use > (uint32_t)stages ? use - stages : 0; u < use; ++u)
-        drain_wait(smem_u32(&bars->full[u % stages]), (u / stages) & 1);
+    if (!ok)  // what is still on its way; the block that was waited for had landed before
+      for (int k = 0; k < filled; ++k, ring.step(stages)) drain_wait(smem_u32(&bars->full[ring.i]), ring.round ^ 1u);
   } else if (warp == 2) {
     // ------------------------------------------------------------ the query
     uint32_t seg = 0;
@@ -219,38 +233,57 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     // ------------------------------------------------------------- the MMAs
     const uint32_t idesc = idesc_bf16_f32(128, Hp, false, false);
     const int per = nlat / a.n_branch;  // latent blocks of a branch
-    uint32_t use = 0, seg = 0;
-    unsigned long long unit0 = 0;  // first unit of the tile
+    RingPos ring, unit;  // the next block; the tile's first score buffer
+    bool lap = false;    // every score buffer has been used
+    uint32_t seg = 0;
     bool ok = true;
-    for (long long i = 0; ok && i < n; ++i, cur.step(), unit0 += a.n_branch) {
+    // block of the query against the ring's block, into score buffer `buf`
+    auto product = [&](int q, int buf, bool add) {
+      if (lane == 0) {
+        const uint64_t td = sdesc_sw128(smem_u32(sT + ring.i * kWtBlock), 16, 1024);
+        const uint64_t qd = sdesc_sw128(smem_u32(sQ + q * q_block), 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ss(tmem + (uint32_t)(buf * stride), td + (uint64_t)(2 * ks), qd + (uint64_t)(2 * ks), idesc,
+                 add || ks ? 1u : 0u);
+      }
+    };
+    auto landed = [&] {
+      ok = mbar_wait_warp(smem_u32(&bars->full[ring.i]), ring.round, abort_flag, err, kWsFull);
+      tc_fence_after();
+      return ok;
+    };
+    auto release = [&] {
+      if (lane == 0) mma_commit(smem_u32(&bars->empty[ring.i]));
+      __syncwarp();
+      ring.step(stages);
+    };
+    for (long long i = 0; ok && i < n; ++i, cur.step()) {
       if (cur.first) {
-        if (!mbar_wait_warp(smem_u32(&bars->q_full), seg & 1, abort_flag, err, kWsQFull)) break;
+        ok = mbar_wait_warp(smem_u32(&bars->q_full), seg & 1, abort_flag, err, kWsQFull);
+        if (!ok) break;
         ++seg;
       }
-      for (int k = 0; ok && k < nblk; ++k, ++use) {
-        const uint32_t s = use % stages;
-        ok = mbar_wait_warp(smem_u32(&bars->full[s]), (use / stages) & 1, abort_flag, err, kWsFull);
+      if (!landed()) break;
+      RingPos u = unit;
+      for (int br = 0; ok && br < a.n_branch; ++br) {  // the rotary part starts every branch
+        if (lap) ok = mbar_wait_warp(smem_u32(&bars->s_free[u.i]), u.round ^ 1u, abort_flag, err, kWsFree);
         if (!ok) break;
-        const uint64_t td = sdesc_sw128(smem_u32(sT + s * kWtBlock), 16, 1024);
-        const uint64_t qd = sdesc_sw128(smem_u32(sQ + (k == 0 ? nlat : k - 1) * q_block), 16, 1024);
-        const int br0 = k == 0 ? 0 : (k - 1) / per, br1 = k == 0 ? a.n_branch : br0 + 1;
-        for (int br = br0; br < br1; ++br) {
-          const unsigned long long u = unit0 + br;
-          const int buf = (int)(u % bufs);
-          if (k == 0 && u >= (unsigned long long)bufs)
-            ok = mbar_wait_warp(smem_u32(&bars->s_free[buf]), (uint32_t)(u / bufs - 1) & 1, abort_flag, err, kWsFree);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem + (uint32_t)(buf * stride), td + (uint64_t)(2 * ks), qd + (uint64_t)(2 * ks), idesc,
-                     (k | ks) ? 1u : 0u);
-            if (k > 0 && (k - 1) % per == per - 1) mma_commit(smem_u32(&bars->s_full[buf]));
-          }
+        tc_fence_after();
+        product(nlat, u.i, false);
+        u.step(bufs);
+        lap = lap || u.i == 0;
+      }
+      if (!ok) break;
+      release();
+      for (int br = 0, k = 0; ok && br < a.n_branch; ++br) {
+        for (int e = 0; e < per; ++e, ++k) {
+          if (!landed()) break;
+          product(k, unit.i, true);
+          if (e + 1 == per && lane == 0) mma_commit(smem_u32(&bars->s_full[unit.i]));
+          release();
         }
-        if (ok && lane == 0) mma_commit(smem_u32(&bars->empty[s]));
-        __syncwarp();
+        unit.step(bufs);
       }
       if (ok && cur.last() && lane == 0) mma_commit(smem_u32(&bars->q_empty));
       __syncwarp();
@@ -268,9 +301,18 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const int row = quarter * 32 + lane;
     const int chunks = Hp / 16, c0 = half ? (chunks + 1) / 2 : 0, c1 = half ? chunks : (chunks + 1) / 2;
-    unsigned long long u = 0;
+    RingPos u;
     uint32_t seg = 0;
-    for (long long i = 0; i < n; ++i, cur.step()) {
+    // weights gathered before, read a tile ahead
+    auto gathered = [&](const TileCursor& c) {
+      const int t = c.t * kWtTile + row;
+      return half == 0 && w_in && c.b < a.B && t < c.L ? w_in[(size_t)c.b * maxL + t] : 0.f;
+    };
+    float before = n > 0 ? gathered(cur) : 0.f;
+    for (long long i = 0; i < n; ++i) {
+      TileCursor next = cur;
+      next.step();
+      const float before_next = i + 1 < n ? gathered(next) : 0.f;
       if (cur.first) {
         // a padded head, and one that attended nothing, add 2^-inf
         float* l = bars->lse[seg & 1];
@@ -285,12 +327,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int t = cur.t * kWtTile + row;
       const size_t at = (size_t)cur.b * maxL + t;
       const bool mine = half == 0 && t < cur.L;
-      const float before = mine && w_in ? w_in[at] : 0.f;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int br = 0; br < a.n_branch; ++br, ++u) {
-        const int buf = (int)(u % bufs);
-        const bool ok = mbar_wait_warp(smem_u32(&bars->s_full[buf]), (uint32_t)(u / bufs) & 1, abort_flag, err,
-                                       kWsScores);
+      for (int br = 0; br < a.n_branch; ++br, u.step(bufs)) {
+        const int buf = u.i;
+        const bool ok = mbar_wait_warp(smem_u32(&bars->s_full[buf]), u.round, abort_flag, err, kWsScores);
         tc_fence_after();
         if (ok) {
           const float* l = bars->lse[(seg - 1) & 1] + br * Hp;
@@ -315,6 +355,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       if (half == 1) bars->half_sum[i & 1][row] = s;
       named_barrier(1, 256);
       if (mine) w_out[at] = before + (s + bars->half_sum[i & 1][row]);
+      before = before_next;
+      cur = next;
     }
   }
   tc_fence_before();
