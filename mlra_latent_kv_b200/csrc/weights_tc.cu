@@ -231,70 +231,66 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     if (*abort_flag && seg > 0) drain_wait(smem_u32(&bars->q_full), (seg - 1) & 1);
   } else if (warp == 1) {
     // ------------------------------------------------------------- the MMAs
-    const uint32_t idesc = idesc_bf16_f32(128, Hp, false, false);
-    const int per = nlat / a.n_branch;  // latent blocks of a branch
-    RingPos ring, unit;  // the next block; the tile's first score buffer
-    bool lap = false;    // every score buffer has been used
-    uint32_t seg = 0;
-    bool ok = true;
-    // block of the query against the ring's block, into score buffer `buf`
-    auto product = [&](int q, int buf, bool add) {
-      if (lane == 0) {
-        const uint64_t td = sdesc_sw128(smem_u32(sT + ring.i * kWtBlock), 16, 1024);
-        const uint64_t qd = sdesc_sw128(smem_u32(sQ + q * q_block), 16, 1024);
+    if (lane == 0) {  // one thread: it waits, issues and commits
+      const uint32_t idesc = idesc_bf16_f32(128, Hp, false, false);
+      const int per = nlat / a.n_branch;  // latent blocks of a branch
+      const uint64_t td0 = sdesc_sw128(smem_u32(sT), 16, 1024), qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      RingPos ring, unit;  // the next block; the tile's first score buffer
+      bool lap = false;    // every score buffer has been used
+      uint32_t seg = 0;
+      bool ok = true;
+      // block q of the query against the ring's block, into score buffer `buf`
+      auto product = [&](int q, int buf, bool add) {
+        const uint64_t td = td0 + (uint64_t)(ring.i * (kWtBlock >> 4)), qd = qd0 + (uint64_t)(q * (q_block >> 4));
+        const uint32_t d = tmem + (uint32_t)(buf * stride);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_ss(tmem + (uint32_t)(buf * stride), td + (uint64_t)(2 * ks), qd + (uint64_t)(2 * ks), idesc,
-                 add || ks ? 1u : 0u);
-      }
-    };
-    auto landed = [&] {
-      ok = mbar_wait_warp(smem_u32(&bars->full[ring.i]), ring.round, abort_flag, err, kWsFull);
-      tc_fence_after();
-      return ok;
-    };
-    auto release = [&] {
-      if (lane == 0) mma_commit(smem_u32(&bars->empty[ring.i]));
-      __syncwarp();
-      ring.step(stages);
-    };
-    for (long long i = 0; ok && i < n; ++i, cur.step()) {
-      if (cur.first) {
-        ok = mbar_wait_warp(smem_u32(&bars->q_full), seg & 1, abort_flag, err, kWsQFull);
-        if (!ok) break;
-        ++seg;
-      }
-      if (!landed()) break;
-      RingPos u = unit;
-      for (int br = 0; ok && br < a.n_branch; ++br) {  // the rotary part starts every branch
-        if (lap) ok = mbar_wait_warp(smem_u32(&bars->s_free[u.i]), u.round ^ 1u, abort_flag, err, kWsFree);
-        if (!ok) break;
+          mma_ss(d, td + (uint64_t)(2 * ks), qd + (uint64_t)(2 * ks), idesc, add || ks ? 1u : 0u);
+      };
+      auto landed = [&] {
+        ok = mbar_wait(smem_u32(&bars->full[ring.i]), ring.round, abort_flag, err, kWsFull);
         tc_fence_after();
-        product(nlat, u.i, false);
-        u.step(bufs);
-        lap = lap || u.i == 0;
-      }
-      if (!ok) break;
-      release();
-      for (int br = 0, k = 0; ok && br < a.n_branch; ++br) {
-        for (int e = 0; e < per; ++e, ++k) {
-          if (!landed()) break;
-          product(k, unit.i, true);
-          if (e + 1 == per && lane == 0) mma_commit(smem_u32(&bars->s_full[unit.i]));
-          release();
+        return ok;
+      };
+      auto release = [&] {
+        mma_commit(smem_u32(&bars->empty[ring.i]));
+        ring.step(stages);
+      };
+      for (long long i = 0; ok && i < n; ++i, cur.step()) {
+        if (cur.first) {
+          ok = mbar_wait(smem_u32(&bars->q_full), seg & 1, abort_flag, err, kWsQFull);
+          if (!ok) break;
+          ++seg;
         }
-        unit.step(bufs);
+        if (!landed()) break;
+        RingPos u = unit;
+        for (int br = 0; ok && br < a.n_branch; ++br) {  // the rotary part starts every branch
+          if (lap) ok = mbar_wait(smem_u32(&bars->s_free[u.i]), u.round ^ 1u, abort_flag, err, kWsFree);
+          if (!ok) break;
+          tc_fence_after();
+          product(nlat, u.i, false);
+          u.step(bufs);
+          lap = lap || u.i == 0;
+        }
+        if (!ok) break;
+        release();
+        for (int br = 0, k = 0; ok && br < a.n_branch; ++br) {
+          for (int e = 0; e < per; ++e, ++k) {
+            if (!landed()) break;
+            product(k, unit.i, true);
+            if (e + 1 == per) mma_commit(smem_u32(&bars->s_full[unit.i]));
+            release();
+          }
+          unit.step(bufs);
+        }
+        if (ok && cur.last()) mma_commit(smem_u32(&bars->q_empty));
       }
-      if (ok && cur.last() && lane == 0) mma_commit(smem_u32(&bars->q_empty));
-      __syncwarp();
-    }
-    if (!ok || *abort_flag) {
-      if (lane == 0) {
+      if (!ok || *abort_flag) {
         mma_commit(smem_u32(&bars->drain));
         drain_wait(smem_u32(&bars->drain), 0);
       }
-      __syncwarp();
     }
+    __syncwarp();
   } else if (warp >= kWtSmx0) {
     // ----------------------------------------------------- the exponentials
     const int quarter = warp & 3, half = (warp - kWtSmx0) >> 2;
