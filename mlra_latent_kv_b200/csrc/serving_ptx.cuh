@@ -14,6 +14,18 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     if (clock64() - t0 > kWaitCycles / 100) return;
 }
 
+// True in one lane of a converged warp; the compiler sees that one thread
+// runs what follows, and keeps an MMA's operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // A barrier among `threads` threads of the CTA (whole warps).
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     if (*abort_flag && seg > 0) drain_wait(smem_u32(&bars->q_full), (seg - 1) & 1);
   } else if (warp == 1) {
     // ------------------------------------------------------------- the MMAs
-    if (lane == 0) {  // one thread: it waits, issues and commits
+    if (elect_one()) {  // one thread: it waits, issues and commits
       const uint32_t idesc = idesc_bf16_f32(128, Hp, false, false);
       const int per = nlat / a.n_branch;  // latent blocks of a branch
       const uint64_t td0 = sdesc_sw128(smem_u32(sT), 16, 1024), qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
