@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const int quarter = warp & 3, half = (warp - kWtSmx0) >> 2;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const int row = quarter * 32 + lane;
-    const int chunks = Hp / 16, c0 = half ? (chunks + 1) / 2 : 0, c1 = half ? chunks : (chunks + 1) / 2;
+    const int mid = (Hp / 16 + 1) / 2 * 16, c0 = half ? mid : 0, c1 = half ? Hp : mid;  // its heads
     RingPos u;
     uint32_t seg = 0;
     // weights gathered before, read a tile ahead
@@ -330,17 +330,27 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         tc_fence_after();
         if (ok) {
           const float* l = bars->lse[(seg - 1) & 1] + br * Hp;
-          for (int c = c0; c < c1; ++c) {
-            uint32_t v[16];
-            tmem_ld16(tmem + lane_off + (uint32_t)(buf * stride + 16 * c), v);
+          const uint32_t col = tmem + lane_off + (uint32_t)(buf * stride);
+          // 2^(v - lse) of four heads from column c on
+          auto add4 = [&](const uint32_t* v, int c) {
+            const float4 r = *reinterpret_cast<const float4*>(l + c);
+            sum[0] += ex2(__uint_as_float(v[0]) - r.x);
+            sum[1] += ex2(__uint_as_float(v[1]) - r.y);
+            sum[2] += ex2(__uint_as_float(v[2]) - r.z);
+            sum[3] += ex2(__uint_as_float(v[3]) - r.w);
+          };
+          int c = c0;
+          for (; c + 32 <= c1; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(col + c, v);
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 r = *reinterpret_cast<const float4*>(l + 16 * c + j);
-              sum[0] += ex2(__uint_as_float(v[j]) - r.x);
-              sum[1] += ex2(__uint_as_float(v[j + 1]) - r.y);
-              sum[2] += ex2(__uint_as_float(v[j + 2]) - r.z);
-              sum[3] += ex2(__uint_as_float(v[j + 3]) - r.w);
-            }
+            for (int j = 0; j < 32; j += 4) add4(v + j, c + j);
+          }
+          if (c < c1) {
+            uint32_t v[16];
+            tmem_ld16(col + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) add4(v + j, c + j);
           }
         }
         tc_fence_before();
