@@ -52,7 +52,7 @@ using namespace ptx;
 
 constexpr int kPtBlock = 128 * 128;  // 128 rows x 64 bf16, or 64 tokens x 128 bf16 as two halves
 constexpr int kPtRing = 8;
-constexpr int kPtThreads = 12 * 32;  // 0 loads, 1 MMAs, 2-3 idle, 4-7 softmax of tile A, 8-11 of tile B
+constexpr int kPtThreads = 12 * 32;  // 0 loads, 1 MMAs, 2 value ends, 3 idle, 4-7 softmax of tile A, 8-11 of tile B
 constexpr int kPtSmem = 6 * kPtBlock + kPtRing * kPtBlock;
 constexpr uint32_t kPtColO = 256;
 constexpr float kPtRescale = 8.f;    // log2
@@ -71,7 +71,7 @@ struct PromptBars {
   uint64_t full[kPtRing], empty[kPtRing];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t item_full[2], item_empty[2];
-  uint64_t drain;
+  uint64_t v_end, v_fixed, drain;  // a value tile with an end has landed; its end is zeroed
   PromptItem item[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -209,8 +209,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       mbar_init(smem_u32(&bars->o_full[x]), 1);
       mbar_init(smem_u32(&bars->o_free[x]), 4);
       mbar_init(smem_u32(&bars->item_full[x]), 1);
-      mbar_init(smem_u32(&bars->item_empty[x]), 9);  // the MMA warp and eight softmax warps
+      mbar_init(smem_u32(&bars->item_empty[x]), 10);  // the MMA thread, warp 2 and eight softmax warps
     }
+    mbar_init(smem_u32(&bars->v_end), 1);
+    mbar_init(smem_u32(&bars->v_fixed), 1);
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort_flag = 0;
     fence_mbar_init();
@@ -356,99 +358,124 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
-    uint32_t base = 0;                                    // ring position of the item's first block
-    uint32_t tiles[2] = {0, 0}, steps[2] = {0, 0};        // query tiles begun, P buffers taken
-    bool ok = true;
-    PromptItem it;
-    for (uint32_t i = 0; ok && take(i, &it) && it.live; ++i) {
-      const int n = max(it.n[0], it.n[1]);
-      auto qk = [&](int x, int j) {
-        const uint32_t kp = base + 5u * j;
-        for (int blk = 0; blk < 3; ++blk) {
-          const uint32_t k = (kp + blk) % kPtRing;
-          ok = ok && mbar_wait_warp(smem_u32(&bars->full[k]), ((kp + blk) / kPtRing) & 1, abort_flag, err, kPsK);
-          if (!ok) return;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t qd = sdesc_sw128(smem_u32(sQ + (3 * x + blk) * kPtBlock), 16, 1024);
-            const uint64_t kd = sdesc_sw128(smem_u32(sR + k * kPtBlock), 16, 1024);
+    if (elect_one()) {  // one thread: it waits, issues and commits
+      uint32_t base = 0;                              // ring position of the item's first block
+      uint32_t tiles[2] = {0, 0}, steps[2] = {0, 0};  // query tiles begun, P buffers taken
+      uint32_t fixes = 0;                             // value tiles whose end was zeroed
+      const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024), kd0 = sdesc_sw128(smem_u32(sR), 16, 1024);
+      const uint64_t vd0 = sdesc_sw128(smem_u32(sR), kPtBlock / 2, 1024);
+      bool ok = true;
+      for (uint32_t i = 0; ok; ++i) {
+        const int sl = i & 1;
+        ok = mbar_wait(smem_u32(&bars->item_full[sl]), (i >> 1) & 1, abort_flag, err, kPsItem);
+        if (!ok) break;
+        const int live = bars->item[sl].live, n0 = bars->item[sl].n[0], n1 = bars->item[sl].n[1], Lk = bars->item[sl].Lk;
+        mbar_arrive(smem_u32(&bars->item_empty[sl]));
+        if (!live) break;
+        const int nx[2] = {n0, n1}, n = max(n0, n1);
+        auto wait_block = [&](uint32_t pos) {
+          ok = ok && mbar_wait(smem_u32(&bars->full[pos % kPtRing]), (pos / kPtRing) & 1, abort_flag, err, kPsK);
+        };
+        auto qk = [&](int x, int j) {
+          const uint32_t kp = base + 5u * j;
+#pragma unroll
+          for (int blk = 0; blk < 3; ++blk) {
+            wait_block(kp + blk);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t qd = qd0 + (uint64_t)((3 * x + blk) * (kPtBlock >> 4));
+            const uint64_t kd = kd0 + (uint64_t)(((kp + blk) % kPtRing) * (kPtBlock >> 4));
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               mma_ss(tmem + 128u * x, qd + (uint64_t)(2 * ks), kd + (uint64_t)(2 * ks), kIdescQK, (blk | ks) ? 1u : 0u);
           }
-          __syncwarp();
-        }
-        if (lane == 0) {
           mma_commit(smem_u32(&bars->s_full[x]));
-          if (x == 1 || j >= it.n[1])  // the last reader of these blocks
+          if (x == 1 || j >= n1)  // the last reader of these blocks
+#pragma unroll
             for (int blk = 0; blk < 3; ++blk) mma_commit(smem_u32(&bars->empty[(kp + blk) % kPtRing]));
-          if (j + 1 == it.n[x]) mma_commit(smem_u32(&bars->q_empty[x]));
-        }
-        __syncwarp();
-      };
-      auto pv = [&](int x, int j) {
-        const uint32_t vp = base + 5u * j + 3u;
-        ok = ok && mbar_wait_warp(smem_u32(&bars->p_full[x]), steps[x] & 1, abort_flag, err, kPsP);
-        // the item before has read its O
-        if (ok && j == 0 && tiles[x] > 1)
-          ok = mbar_wait_warp(smem_u32(&bars->o_free[x]), (tiles[x] - 2) & 1, abort_flag, err, kPsOFree);
-        if (!ok) return;
-        ++steps[x];
-        const int rows = it.Lk - 128 * j;               // value rows inside the sequence
-        const bool first = x == 0 || j >= it.n[0];      // the first reader of these blocks
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t k = (vp + half) % kPtRing;
-          ok = mbar_wait_warp(smem_u32(&bars->full[k]), ((vp + half) / kPtRing) & 1, abort_flag, err, kPsV);
-          if (!ok) return;
-          uint8_t* blk = sR + k * kPtBlock;
-          const int have = rows - 64 * half;
-          if (first && have < 64) {
-            const int r0 = max(0, have), nz = (64 - r0) * 8;
-            for (int e = lane; e < 2 * nz; e += 32)
-              *reinterpret_cast<uint4*>(blk + (e / nz) * (kPtBlock / 2) + r0 * 128 + (e % nz) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
+          if (j + 1 == nx[x]) mma_commit(smem_u32(&bars->q_empty[x]));
+        };
+        auto pv = [&](int x, int j) {
+          const uint32_t vp = base + 5u * j + 3u;
+          const bool end = (x == 0 || j >= n0) && Lk < 128 * (j + 1);  // the first reader of a value tile with an end
+          if (end) {  // warp 2 zeroes it while the softmax runs
+            wait_block(vp);
+            wait_block(vp + 1);
+            if (ok) mbar_arrive(smem_u32(&bars->v_end));
           }
-          __syncwarp();
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t vd = sdesc_sw128(smem_u32(blk), kPtBlock / 2, 1024);
+          ok = ok && mbar_wait(smem_u32(&bars->p_full[x]), steps[x] & 1, abort_flag, err, kPsP);
+          if (end) {
+            ok = ok && mbar_wait(smem_u32(&bars->v_fixed), fixes & 1, abort_flag, err, kPsV);
+            ++fixes;
+          }
+          // the item before has read its O
+          if (j == 0 && tiles[x] > 1)
+            ok = ok && mbar_wait(smem_u32(&bars->o_free[x]), (tiles[x] - 2) & 1, abort_flag, err, kPsOFree);
+          ++steps[x];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            wait_block(vp + half);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t vd = vd0 + (uint64_t)(((vp + half) % kPtRing) * (kPtBlock >> 4));
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               mma_ts(tmem + kPtColO + 128u * x, tmem + 128u * x + 32u * half + 8u * ks,
                      vd + (uint64_t)((ks * 2048) >> 4), kIdescPV, (j | half | ks) ? 1u : 0u);
           }
-          __syncwarp();
-        }
-        if (lane == 0) {
-          if (x == 1 || j >= it.n[1]) {
+          if (x == 1 || j >= n1) {
             mma_commit(smem_u32(&bars->empty[vp % kPtRing]));
             mma_commit(smem_u32(&bars->empty[(vp + 1) % kPtRing]));
           }
-          if (j + 1 == it.n[x]) mma_commit(smem_u32(&bars->o_full[x]));
+          if (j + 1 == nx[x]) mma_commit(smem_u32(&bars->o_full[x]));
+        };
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (nx[x] == 0) continue;
+          ok = ok && mbar_wait(smem_u32(&bars->q_full[x]), tiles[x] & 1, abort_flag, err, kPsQ);
+          ++tiles[x];
+          if (ok) qk(x, 0);
         }
-        __syncwarp();
-      };
-      for (int x = 0; ok && x < 2; ++x) {
-        if (it.n[x] == 0) continue;
-        ok = mbar_wait_warp(smem_u32(&bars->q_full[x]), tiles[x] & 1, abort_flag, err, kPsQ);
-        ++tiles[x];
-        if (ok) qk(x, 0);
+        for (int j = 0; ok && j < n; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || j >= nx[x]) continue;
+            pv(x, j);
+            if (ok && j + 1 < nx[x]) qk(x, j + 1);
+          }
+        base += 5u * n;
       }
-      for (int j = 0; ok && j < n; ++j)
-        for (int x = 0; ok && x < 2; ++x) {
-          if (j >= it.n[x]) continue;
-          pv(x, j);
-          if (ok && j + 1 < it.n[x]) qk(x, j + 1);
-        }
-      base += 5u * n;
-    }
-    if (*abort_flag) {
-      if (lane == 0) {
+      if (*abort_flag) {
         mma_commit(smem_u32(&bars->drain));
         drain_wait(smem_u32(&bars->drain), 0);
       }
-      __syncwarp();
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------ value rows past a sequence's end
+    uint32_t base = 0, fixes = 0;
+    bool ok = true;
+    PromptItem it;
+    for (uint32_t i = 0; ok && take(i, &it) && it.live; ++i) {
+      const int n = max(it.n[0], it.n[1]);
+      const int rows = it.Lk - 128 * (n - 1);  // of the item's last value tile, inside the sequence
+      if (n > 0 && rows < 128) {
+        ok = mbar_wait_warp(smem_u32(&bars->v_end), fixes & 1, abort_flag, err, kPsV);
+        for (int half = 0; ok && half < 2; ++half) {
+          const uint32_t pos = base + 5u * (n - 1) + 3u + half;
+          const int r0 = max(0, rows - 64 * half), nz = (64 - r0) * 8;  // 16-byte pieces of each half of the dims
+          uint8_t* blk = sR + (pos % kPtRing) * kPtBlock + r0 * 128;
+          for (int e = lane; e < nz; e += 32)
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+              *reinterpret_cast<uint4*>(blk + d * (kPtBlock / 2) + e * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(smem_u32(&bars->v_fixed));
+        ++fixes;
+      }
+      base += 5u * n;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------- softmax
