@@ -24,6 +24,10 @@ NVCC_FLAGS = [
     "--expt-relaxed-constexpr",
 ]
 
+# Compiled as a whole program: ptxas deals registers to a kernel's warp roles
+# (setmaxnreg) only where it sees every caller of the kernel's code.
+WHOLE_PROGRAM = {"prompt_tc.cu"}
+
 
 def nvcc() -> str:
     for cand in (os.environ.get("NVCC"), "/usr/local/cuda/bin/nvcc", shutil.which("nvcc")):
@@ -59,8 +63,8 @@ def build(force: bool = False, verbose: bool = False, out: str | None = None, de
     objs = []
     for src in sources():
         obj = os.path.join(bdir, os.path.basename(src) + ".o")
-        cmd = [nvcc(), *NVCC_FLAGS, *[f"-D{d}" for d in defines], "-I", os.path.join(ROOT, "include"), "-dc", src,
-               "-o", obj]
+        cmd = [nvcc(), *NVCC_FLAGS, *[f"-D{d}" for d in defines], "-I", os.path.join(ROOT, "include"),
+               "-c" if os.path.basename(src) in WHOLE_PROGRAM else "-dc", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)

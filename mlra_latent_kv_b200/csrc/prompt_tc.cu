@@ -40,6 +40,8 @@
 //     copies and MMAs in flight end and leaves.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "host_cache.h"
 #include "launch.h"
 #include "serving.h"
@@ -52,10 +54,12 @@ using namespace ptx;
 
 constexpr int kPtBlock = 128 * 128;  // 128 rows x 64 bf16, or 64 tokens x 128 bf16 as two halves
 constexpr int kPtRing = 8;
-constexpr int kPtThreads = 12 * 32;  // 0 loads, 1 MMAs, 2 value ends, 3 idle, 4-7 softmax of tile A, 8-11 of tile B
+constexpr int kPtThreads = 12 * 32;  // 0 loads, 1 and 3 MMAs, 2 value ends, 4-7 softmax of tile A, 8-11 of tile B
 constexpr int kPtSmem = 6 * kPtBlock + kPtRing * kPtBlock;
 constexpr uint32_t kPtColO = 256;
 constexpr float kPtRescale = 8.f;    // log2
+constexpr int kPtRegs = 168, kPtRegsAux = 88, kPtRegsSoftmax = 208;  // of a thread: at launch, then by role
+static_assert(4 * kPtRegsAux + 8 * kPtRegsSoftmax <= 12 * kPtRegs, "the roles share the registers of the launch");
 constexpr int kPlanThreads = 512;
 constexpr int kPlanBins = 1024;
 
@@ -71,13 +75,15 @@ struct PromptBars {
   uint64_t full[kPtRing], empty[kPtRing];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t item_full[2], item_empty[2];
-  uint64_t v_end, v_fixed, drain;  // a value tile with an end has landed; its end is zeroed
+  uint64_t v_fixed[2];  // a value tile's end is zeroed; in turn, for the ring may hold two such tiles
+  uint64_t turn[2];     // the other tile has issued its step
+  uint64_t drain[2];
   PromptItem item[2];
   uint32_t tmem_base;
   int abort_flag;
 };
 
-enum { kPsRing = 60, kPsItem, kPsItemFree, kPsQ, kPsQFree, kPsK, kPsV, kPsP, kPsOFree, kPsS, kPsO };
+enum { kPsRing = 60, kPsItem, kPsItemFree, kPsQ, kPsQFree, kPsK, kPsV, kPsP, kPsOFree, kPsS, kPsO, kPsTurn };
 
 // ---------------------------------------------------------------------------
 // Plan and query rotation.  Block 0 checks the sequences and lists the pairs
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   if (threadIdx.x == 0) {
     for (int k = 0; k < kPtRing; ++k) {
       mbar_init(smem_u32(&bars->full[k]), 1);
-      mbar_init(smem_u32(&bars->empty[k]), 1);
+      mbar_init(smem_u32(&bars->empty[k]), 3);  // both tiles' MMAs and the value ends' warp
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&bars->q_full[x]), 1);
@@ -208,12 +214,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       mbar_init(smem_u32(&bars->p_full[x]), 4);
       mbar_init(smem_u32(&bars->o_full[x]), 1);
       mbar_init(smem_u32(&bars->o_free[x]), 4);
+      mbar_init(smem_u32(&bars->v_fixed[x]), 1);
+      mbar_init(smem_u32(&bars->turn[x]), 1);
+      mbar_init(smem_u32(&bars->drain[x]), 1);
       mbar_init(smem_u32(&bars->item_full[x]), 1);
-      mbar_init(smem_u32(&bars->item_empty[x]), 10);  // the MMA thread, warp 2 and eight softmax warps
+      mbar_init(smem_u32(&bars->item_empty[x]), 11);  // the MMA threads, warp 2 and eight softmax warps
     }
-    mbar_init(smem_u32(&bars->v_end), 1);
-    mbar_init(smem_u32(&bars->v_fixed), 1);
-    mbar_init(smem_u32(&bars->drain), 1);
     bars->abort_flag = 0;
     fence_mbar_init();
   }
@@ -236,6 +242,153 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     return true;
   };
 
+  // The launch's registers, dealt out anew.  Each half of the roles stands wholly behind its own instruction.
+  if (warp >= 4) {
+    setmaxnreg_inc<kPtRegsSoftmax>();
+    // ------------------------------------------------------------- softmax
+    const int x = (warp - 4) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_col = tmem + lane_off + 128u * x, o_col = tmem + lane_off + kPtColO + 128u * x;
+    const float sc = a.scale_log2, jump = kPtRescale / sc;
+    uint32_t steps = 0, tiles = 0;
+    bool ok = true;
+    PromptItem it;
+    for (uint32_t i = 0; ok && take(i, &it) && it.live; ++i) {
+      const int tok = it.tok0 + x * TT + row / pack, head = it.head0 + row % pack;
+      const bool mine = tok < it.Lq;
+      const int n = it.n[x];
+      const int lim = min(it.Lk - it.Lq + tok, it.Lk - 1);  // the row's last key
+      const size_t at = (size_t)(it.q0 + tok) * a.H + head;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++steps) {
+        ok = mbar_wait_warp(smem_u32(&bars->s_full[x]), steps & 1, abort_flag, err, kPsS);
+        if (!ok) break;
+        tc_fence_after();
+        const int cmax = lim - 128 * j;
+        const bool masked = __any_sync(0xffffffffu, cmax < 127);
+        // scores c0 .. c0 + 63 of the row, -inf past its last key
+        auto load = [&](auto ends, int c0, uint32_t (&v)[32], uint32_t (&w)[32]) {
+          tmem_ld32x2(s_col + c0, s_col + c0 + 32, v, w);
+          if constexpr (decltype(ends)::value) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              if (c0 + c > cmax) v[c] = 0xff800000u;
+              if (c0 + 32 + c > cmax) w[c] = 0xff800000u;
+            }
+          }
+        };
+        auto largest = [&](float t, const uint32_t (&v)[32]) {
+          float t0 = t, t1 = __uint_as_float(v[0]);
+#pragma unroll
+          for (int c = 1; c < 31; c += 3) {
+            t0 = fmaxf(fmaxf(t0, __uint_as_float(v[c])), __uint_as_float(v[c + 1]));
+            t1 = fmaxf(t1, __uint_as_float(v[c + 2]));
+          }
+          return fmaxf(fmaxf(t0, t1), __uint_as_float(v[31]));
+        };
+        uint32_t p[4][16];  // P of 32 keys each, packed
+        float top, sum;
+        auto exponentials = [&](auto ends) {
+          const float ref = m == -INFINITY ? 0.f : -m * sc;  // no key so far: every term is 2^-inf = 0
+          const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(ref, ref);
+          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          top = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[2][32];
+            load(ends, 64 * h, v[0], v[1]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              top = largest(top, v[g]);
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                float2 e = fma_f32x2(make_float2(__uint_as_float(v[g][2 * u]), __uint_as_float(v[g][2 * u + 1])), sc2,
+                                     ref2);
+                e.x = ex2(e.x);
+                e.y = ex2(e.y);
+                s2[u & 1] = add_f32x2(s2[u & 1], e);
+                p[2 * h + g][u] = pack_bf16x2(e.x, e.y);
+              }
+            }
+          }
+          sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+        };
+        if (j == 0) {
+          m = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[32], w[32];
+            load(std::true_type(), 64 * h, v, w);
+            m = largest(largest(m, v), w);
+          }
+        }
+        // against the maximum so far; the scores stay where they are until it is known that this will do
+        if (masked)
+          exponentials(std::true_type());
+        else
+          exponentials(std::false_type());
+        if (j > 0 && __any_sync(0xffffffffu, top > m + jump)) {
+          float corr = 1.f;
+          if (top > m + jump) {
+            corr = ex2((m - top) * sc);
+            m = top;
+          }
+          l *= corr;
+          exponentials(std::true_type());
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_col + c, o);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * corr);
+            tmem_st16(o_col + c, o);
+          }
+        }
+        l += sum;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) tmem_st16_async(s_col + 16u * g, p[g]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[x]));
+      }
+      if (!ok) break;
+      if (n > 0) {
+        ok = mbar_wait_warp(smem_u32(&bars->o_full[x]), tiles & 1, abort_flag, err, kPsO);
+        ++tiles;
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      __nv_bfloat16* dst = out + at * 128;
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        if (n > 0) tmem_ld32(o_col + c, o);
+        if (mine) {
+#pragma unroll
+          for (int u = 0; u < 32; u += 8) {
+            uint4 pk = make_uint4(0, 0, 0, 0);
+            if (l != 0.f) {
+              pk.x = pack_bf16x2(__uint_as_float(o[u]) * inv, __uint_as_float(o[u + 1]) * inv);
+              pk.y = pack_bf16x2(__uint_as_float(o[u + 2]) * inv, __uint_as_float(o[u + 3]) * inv);
+              pk.z = pack_bf16x2(__uint_as_float(o[u + 4]) * inv, __uint_as_float(o[u + 5]) * inv);
+              pk.w = pack_bf16x2(__uint_as_float(o[u + 6]) * inv, __uint_as_float(o[u + 7]) * inv);
+            }
+            *reinterpret_cast<uint4*>(dst + c + u) = pk;
+          }
+        }
+      }
+      if (n > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->o_free[x]));
+      }
+      if (lse && mine) lse[at] = l == 0.f ? -INFINITY : m * sc + log2f(l);
+    }
+  } else {
+    setmaxnreg_dec<kPtRegsAux>();
   if (warp == 0) {
     // --------------------------------------------------------------- loads
     if (lane == 0) {
@@ -356,15 +509,25 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       for (int x = 0; x < 2; ++x)
         if (tiles[x] > 0) drain_wait(smem_u32(&bars->q_full[x]), (tiles[x] - 1) & 1);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 3) {
     // ---------------------------------------------------------------- MMAs
-    if (elect_one()) {  // one thread: it waits, issues and commits
-      uint32_t base = 0;                              // ring position of the item's first block
-      uint32_t tiles[2] = {0, 0}, steps[2] = {0, 0};  // query tiles begun, P buffers taken
-      uint32_t fixes = 0;                             // value tiles whose end was zeroed
-      const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024), kd0 = sdesc_sw128(smem_u32(sR), 16, 1024);
-      const uint64_t vd0 = sdesc_sw128(smem_u32(sR), kPtBlock / 2, 1024);
-      bool ok = true;
+    // One thread per tile waits, issues and commits: QK^T of step j + 1 right behind PV of step j, which
+    // reads the P that lies where the new scores go.  A thread's wait drains the tensor pipe of its own
+    // MMAs; the other tile's keep it busy.  The tiles take turns, so that one's softmax falls into the
+    // other's products.
+    if (elect_one()) {
+      const int x = warp >> 1;
+      uint32_t base = 0;               // ring position of the item's first block
+      uint32_t tiles = 0, steps = 0;   // query tiles begun, P buffers taken
+      uint32_t ends = 0, turns = 0;    // value tiles with an end, turns taken
+      const uint64_t qd0 = sdesc_sw128(smem_u32(sQ + 3 * x * kPtBlock), 16, 1024);
+      const uint64_t kd0 = sdesc_sw128(smem_u32(sR), 16, 1024), vd0 = sdesc_sw128(smem_u32(sR), kPtBlock / 2, 1024);
+      const uint32_t s_col = tmem + 128u * x, o_col = tmem + kPtColO + 128u * x;
+      bool ok = true, owed = false;
+      auto wait_block = [&](uint32_t pos) {
+        ok = ok && mbar_wait(smem_u32(&bars->full[pos % kPtRing]), (pos / kPtRing) & 1, abort_flag, err, kPsK);
+      };
+      auto block = [&](uint32_t pos) { return (uint64_t)((pos % kPtRing) * (kPtBlock >> 4)); };
       for (uint32_t i = 0; ok; ++i) {
         const int sl = i & 1;
         ok = mbar_wait(smem_u32(&bars->item_full[sl]), (i >> 1) & 1, abort_flag, err, kPsItem);
@@ -372,251 +535,113 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int live = bars->item[sl].live, n0 = bars->item[sl].n[0], n1 = bars->item[sl].n[1], Lk = bars->item[sl].Lk;
         mbar_arrive(smem_u32(&bars->item_empty[sl]));
         if (!live) break;
-        const int nx[2] = {n0, n1}, n = max(n0, n1);
-        auto wait_block = [&](uint32_t pos) {
-          ok = ok && mbar_wait(smem_u32(&bars->full[pos % kPtRing]), (pos / kPtRing) & 1, abort_flag, err, kPsK);
+        const int mine = x ? n1 : n0, n = max(n0, n1);
+        auto wait_keys = [&](int j) {
+#pragma unroll
+          for (int blk = 0; blk < 3; ++blk) wait_block(base + 5u * j + blk);
         };
-        auto qk = [&](int x, int j) {
+        auto qk = [&](int j) {
           const uint32_t kp = base + 5u * j;
 #pragma unroll
-          for (int blk = 0; blk < 3; ++blk) {
-            wait_block(kp + blk);
-            if (!ok) return;
-            tc_fence_after();
-            const uint64_t qd = qd0 + (uint64_t)((3 * x + blk) * (kPtBlock >> 4));
-            const uint64_t kd = kd0 + (uint64_t)(((kp + blk) % kPtRing) * (kPtBlock >> 4));
+          for (int blk = 0; blk < 3; ++blk)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem + 128u * x, qd + (uint64_t)(2 * ks), kd + (uint64_t)(2 * ks), kIdescQK, (blk | ks) ? 1u : 0u);
-          }
+              mma_ss(s_col, qd0 + (uint64_t)(blk * (kPtBlock >> 4) + 2 * ks), kd0 + block(kp + blk) + (uint64_t)(2 * ks),
+                     kIdescQK, (blk | ks) ? 1u : 0u);
           mma_commit(smem_u32(&bars->s_full[x]));
-          if (x == 1 || j >= n1)  // the last reader of these blocks
 #pragma unroll
-            for (int blk = 0; blk < 3; ++blk) mma_commit(smem_u32(&bars->empty[(kp + blk) % kPtRing]));
-          if (j + 1 == nx[x]) mma_commit(smem_u32(&bars->q_empty[x]));
+          for (int blk = 0; blk < 3; ++blk) mma_commit(smem_u32(&bars->empty[(kp + blk) % kPtRing]));
+          if (j + 1 == mine) mma_commit(smem_u32(&bars->q_empty[x]));
         };
-        auto pv = [&](int x, int j) {
+        auto pv = [&](int j) {
           const uint32_t vp = base + 5u * j + 3u;
-          const bool end = (x == 0 || j >= n0) && Lk < 128 * (j + 1);  // the first reader of a value tile with an end
-          if (end) {  // warp 2 zeroes it while the softmax runs
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ts(o_col, s_col + 32u * half + 8u * ks, vd0 + block(vp + half) + (uint64_t)((ks * 2048) >> 4), kIdescPV,
+                     (j | half | ks) ? 1u : 0u);
+          mma_commit(smem_u32(&bars->empty[vp % kPtRing]));
+          mma_commit(smem_u32(&bars->empty[(vp + 1) % kPtRing]));
+          if (j + 1 == mine) mma_commit(smem_u32(&bars->o_full[x]));
+        };
+        if (mine > 0) {
+          ok = mbar_wait(smem_u32(&bars->q_full[x]), tiles & 1, abort_flag, err, kPsQ);
+          ++tiles;
+          wait_keys(0);
+          if (ok) {
+            tc_fence_after();
+            qk(0);
+          }
+          for (int j = 0; ok && j < mine; ++j, ++steps) {
+            // everything that the step needs, so that no wait stands between its MMAs; P comes last
+            const uint32_t vp = base + 5u * j + 3u;
             wait_block(vp);
             wait_block(vp + 1);
-            if (ok) mbar_arrive(smem_u32(&bars->v_end));
-          }
-          ok = ok && mbar_wait(smem_u32(&bars->p_full[x]), steps[x] & 1, abort_flag, err, kPsP);
-          if (end) {
-            ok = ok && mbar_wait(smem_u32(&bars->v_fixed), fixes & 1, abort_flag, err, kPsV);
-            ++fixes;
-          }
-          // the item before has read its O
-          if (j == 0 && tiles[x] > 1)
-            ok = ok && mbar_wait(smem_u32(&bars->o_free[x]), (tiles[x] - 2) & 1, abort_flag, err, kPsOFree);
-          ++steps[x];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            wait_block(vp + half);
-            if (!ok) return;
+            if (j + 1 < mine) wait_keys(j + 1);
+            if (Lk < 128 * (j + 1))
+              ok = ok && mbar_wait(smem_u32(&bars->v_fixed[ends & 1]), (ends >> 1) & 1, abort_flag, err, kPsV);
+            if (j == 0 && tiles > 1)  // the item before has read its O
+              ok = ok && mbar_wait(smem_u32(&bars->o_free[x]), (tiles - 2) & 1, abort_flag, err, kPsOFree);
+            if (x ? j < n0 : owed)  // strictly in turn: no token is passed before the last one was taken
+              ok = ok && mbar_wait(smem_u32(&bars->turn[x]), turns++ & 1, abort_flag, err, kPsTurn);
+            ok = ok && mbar_wait(smem_u32(&bars->p_full[x]), steps & 1, abort_flag, err, kPsP);
+            if (!ok) break;
             tc_fence_after();
-            const uint64_t vd = vd0 + (uint64_t)(((vp + half) % kPtRing) * (kPtBlock >> 4));
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_ts(tmem + kPtColO + 128u * x, tmem + 128u * x + 32u * half + 8u * ks,
-                     vd + (uint64_t)((ks * 2048) >> 4), kIdescPV, (j | half | ks) ? 1u : 0u);
+            pv(j);
+            if (j + 1 < mine) qk(j + 1);
+            owed = j < (x ? n0 : n1);  // the other tile has this step too
+            if (owed) mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
           }
-          if (x == 1 || j >= n1) {
-            mma_commit(smem_u32(&bars->empty[vp % kPtRing]));
-            mma_commit(smem_u32(&bars->empty[(vp + 1) % kPtRing]));
-          }
-          if (j + 1 == nx[x]) mma_commit(smem_u32(&bars->o_full[x]));
-        };
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (nx[x] == 0) continue;
-          ok = ok && mbar_wait(smem_u32(&bars->q_full[x]), tiles[x] & 1, abort_flag, err, kPsQ);
-          ++tiles[x];
-          if (ok) qk(x, 0);
         }
-        for (int j = 0; ok && j < n; ++j)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || j >= nx[x]) continue;
-            pv(x, j);
-            if (ok && j + 1 < nx[x]) qk(x, j + 1);
-          }
+        // blocks that only the other tile reads: passed on as they come
+        for (uint32_t pos = base + 5u * mine; ok && pos < base + 5u * n; ++pos) {
+          wait_block(pos);
+          if (ok) mbar_arrive(smem_u32(&bars->empty[pos % kPtRing]));
+        }
         base += 5u * n;
+        ends += n > 0 && Lk < 128 * n;
       }
       if (*abort_flag) {
-        mma_commit(smem_u32(&bars->drain));
-        drain_wait(smem_u32(&bars->drain), 0);
+        mma_commit(smem_u32(&bars->drain[x]));
+        drain_wait(smem_u32(&bars->drain[x]), 0);
       }
     }
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------ value rows past a sequence's end
-    uint32_t base = 0, fixes = 0;
+    // Follows the ring block by block; a value block with an end is zeroed behind it.
+    uint32_t pos = 0, ends = 0;
     bool ok = true;
     PromptItem it;
     for (uint32_t i = 0; ok && take(i, &it) && it.live; ++i) {
       const int n = max(it.n[0], it.n[1]);
-      const int rows = it.Lk - 128 * (n - 1);  // of the item's last value tile, inside the sequence
-      if (n > 0 && rows < 128) {
-        ok = mbar_wait_warp(smem_u32(&bars->v_end), fixes & 1, abort_flag, err, kPsV);
-        for (int half = 0; ok && half < 2; ++half) {
-          const uint32_t pos = base + 5u * (n - 1) + 3u + half;
-          const int r0 = max(0, rows - 64 * half), nz = (64 - r0) * 8;  // 16-byte pieces of each half of the dims
-          uint8_t* blk = sR + (pos % kPtRing) * kPtBlock + r0 * 128;
-          for (int e = lane; e < nz; e += 32)
+      for (int j = 0; ok && j < n; ++j) {
+        const int rows = it.Lk - 128 * j;  // of the value tile, inside the sequence
+        for (int blk = 0; ok && blk < 5; ++blk, ++pos) {
+          const uint32_t k = pos % kPtRing;
+          ok = mbar_wait_warp(smem_u32(&bars->full[k]), (pos / kPtRing) & 1, abort_flag, err, kPsV);
+          if (!ok) break;
+          const int have = rows - 64 * (blk - 3);
+          if (blk >= 3 && have < 64) {
+            const int r0 = max(0, have), nz = (64 - r0) * 8;  // 16-byte pieces of each half of the dims
+            uint8_t* to = sR + k * kPtBlock + r0 * 128;
+            for (int e = lane; e < nz; e += 32)
 #pragma unroll
-            for (int d = 0; d < 2; ++d)
-              *reinterpret_cast<uint4*>(blk + d * (kPtBlock / 2) + e * 16) = make_uint4(0, 0, 0, 0);
+              for (int d = 0; d < 2; ++d)
+                *reinterpret_cast<uint4*>(to + d * (kPtBlock / 2) + e * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->empty[k]));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(smem_u32(&bars->v_fixed));
-        ++fixes;
+        if (ok && rows < 128) {  // the sequence's last value tile
+          if (lane == 0) mbar_arrive(smem_u32(&bars->v_fixed[ends & 1]));
+          ++ends;
+        }
       }
-      base += 5u * n;
     }
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------- softmax
-    const int x = (warp - 4) >> 2, quarter = warp & 3;
-    const int row = quarter * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_col = tmem + lane_off + 128u * x, o_col = tmem + lane_off + kPtColO + 128u * x;
-    const float sc = a.scale_log2, jump = kPtRescale / sc;
-    uint32_t steps = 0, tiles = 0;
-    bool ok = true;
-    PromptItem it;
-    for (uint32_t i = 0; ok && take(i, &it) && it.live; ++i) {
-      const int tok = it.tok0 + x * TT + row / pack, head = it.head0 + row % pack;
-      const bool mine = tok < it.Lq;
-      const int n = it.n[x];
-      const int lim = min(it.Lk - it.Lq + tok, it.Lk - 1);  // the row's last key
-      const size_t at = (size_t)(it.q0 + tok) * a.H + head;
-      float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j, ++steps) {
-        ok = mbar_wait_warp(smem_u32(&bars->s_full[x]), steps & 1, abort_flag, err, kPsS);
-        if (!ok) break;
-        tc_fence_after();
-        const int cmax = lim - 128 * j;
-        const bool masked = __any_sync(0xffffffffu, cmax < 127);
-        // scores c0 .. c0 + 63 of the row, -inf past its last key
-        auto load = [&](int c0, uint32_t (&v)[32], uint32_t (&w)[32]) {
-          tmem_ld32x2(s_col + c0, s_col + c0 + 32, v, w);
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (c0 + c > cmax) v[c] = 0xff800000u;
-              if (c0 + 32 + c > cmax) w[c] = 0xff800000u;
-            }
-          }
-        };
-        auto largest = [&](float t, const uint32_t (&v)[32]) {
-          float t0 = t, t1 = __uint_as_float(v[0]);
-#pragma unroll
-          for (int c = 1; c < 31; c += 3) {
-            t0 = fmaxf(fmaxf(t0, __uint_as_float(v[c])), __uint_as_float(v[c + 1]));
-            t1 = fmaxf(t1, __uint_as_float(v[c + 2]));
-          }
-          return fmaxf(fmaxf(t0, t1), __uint_as_float(v[31]));
-        };
-        uint32_t p[4][16];  // P of 32 keys each, packed
-        float top, sum;
-        auto exponentials = [&] {
-          const float ref = m == -INFINITY ? 0.f : -m * sc;  // no key so far: every term is 2^-inf = 0
-          const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(ref, ref);
-          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          top = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[2][32];
-            load(64 * h, v[0], v[1]);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              top = largest(top, v[g]);
-#pragma unroll
-              for (int u = 0; u < 16; ++u) {
-                float2 e = fma_f32x2(make_float2(__uint_as_float(v[g][2 * u]), __uint_as_float(v[g][2 * u + 1])), sc2,
-                                     ref2);
-                e.x = ex2(e.x);
-                e.y = ex2(e.y);
-                s2[u & 1] = add_f32x2(s2[u & 1], e);
-                p[2 * h + g][u] = pack_bf16x2(e.x, e.y);
-              }
-            }
-          }
-          sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-        };
-        if (j == 0) {
-          m = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[32], w[32];
-            load(64 * h, v, w);
-            m = largest(largest(m, v), w);
-          }
-        }
-        // against the maximum so far; the scores stay where they are until it is known that this will do
-        exponentials();
-        if (j > 0 && __any_sync(0xffffffffu, top > m + jump)) {
-          float corr = 1.f;
-          if (top > m + jump) {
-            corr = ex2((m - top) * sc);
-            m = top;
-          }
-          l *= corr;
-          exponentials();
-#pragma unroll
-          for (int c = 0; c < 128; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(o_col + c, o);
-#pragma unroll
-            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * corr);
-            tmem_st16(o_col + c, o);
-          }
-        }
-        l += sum;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) tmem_st16_async(s_col + 16u * g, p[g]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[x]));
-      }
-      if (!ok) break;
-      if (n > 0) {
-        ok = mbar_wait_warp(smem_u32(&bars->o_full[x]), tiles & 1, abort_flag, err, kPsO);
-        ++tiles;
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      __nv_bfloat16* dst = out + at * 128;
-#pragma unroll
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t o[32];
-        if (n > 0) tmem_ld32(o_col + c, o);
-        if (mine) {
-#pragma unroll
-          for (int u = 0; u < 32; u += 8) {
-            uint4 pk = make_uint4(0, 0, 0, 0);
-            if (l != 0.f) {
-              pk.x = pack_bf16x2(__uint_as_float(o[u]) * inv, __uint_as_float(o[u + 1]) * inv);
-              pk.y = pack_bf16x2(__uint_as_float(o[u + 2]) * inv, __uint_as_float(o[u + 3]) * inv);
-              pk.z = pack_bf16x2(__uint_as_float(o[u + 4]) * inv, __uint_as_float(o[u + 5]) * inv);
-              pk.w = pack_bf16x2(__uint_as_float(o[u + 6]) * inv, __uint_as_float(o[u + 7]) * inv);
-            }
-            *reinterpret_cast<uint4*>(dst + c + u) = pk;
-          }
-        }
-      }
-      if (n > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->o_free[x]));
-      }
-      if (lse && mine) lse[at] = l == 0.f ? -INFINITY : m * sc + log2f(l);
-    }
+  }
   }
   tc_fence_before();
   __syncthreads();
@@ -688,6 +713,12 @@ cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* 
   const long long bytes = (long long)a.total_k * 512 * a.kv_heads / units;
   long long group = bytes > 0 ? (48LL << 20) / bytes : units;
   group = group < 1 ? 1 : (group > units ? units : group);
+  // what the roles are dealt has to be there: the kernel's registers at launch
+  static const int regs = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, prompt_tc_kernel) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (regs != kPtRegs) return cudaErrorInvalidConfiguration;
   const int smem = 1024 + kPtSmem + (int)sizeof(PromptBars);
   e = ensure_smem(reinterpret_cast<const void*>(prompt_tc_kernel), smem);
   if (e != cudaSuccess) return e;

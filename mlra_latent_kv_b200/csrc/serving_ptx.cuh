@@ -14,6 +14,16 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     if (clock64() - t0 > kWaitCycles / 100) return;
 }
 
+// Registers per thread from here on, for every warp of a warpgroup alike.
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // True in one lane of a converged warp; the compiler sees that one thread
 // runs what follows, and keeps an MMA's operands in uniform registers.
 __device__ __forceinline__ bool elect_one() {
