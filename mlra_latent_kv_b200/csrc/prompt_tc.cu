@@ -23,8 +23,8 @@
 //     While one tile's softmax runs, the tensor cores work on the other:
 //     PV and the next QK^T of tile A, then of tile B.
 //   * Shared memory: the two query tiles (96 KB) and a ring of eight 16 KB
-//     blocks (a key tile of 128 tokens is three of 64 dims, a value tile two of
-//     64 tokens), so that loads run more than a tile ahead.
+//     blocks; a step's keys (128 tokens) are three of 64 dims, its values two of
+//     64 tokens, so that 1.6 steps are loaded or on their way.
 //   * Softmax: a thread per row, running maximum and sum in fp32, base 2.  The
 //     exponentials are taken against the maximum so far, in the same pass that
 //     finds the step's own, with P held back in registers; only when a row's
@@ -72,7 +72,7 @@ struct PromptItem {
 };
 
 struct PromptBars {
-  uint64_t full[kPtRing], empty[kPtRing];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // of step t: t % 2
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t item_full[2], item_empty[2];
   uint64_t v_fixed[2];  // a value tile's end is zeroed; in turn, for the ring may hold two such tiles
@@ -203,11 +203,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const int TT = 128 / pack;
 
   if (threadIdx.x == 0) {
-    for (int k = 0; k < kPtRing; ++k) {
-      mbar_init(smem_u32(&bars->full[k]), 1);
-      mbar_init(smem_u32(&bars->empty[k]), 3);  // both tiles' MMAs and the value ends' warp
-    }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_u32(&bars->k_full[x]), 1);
+      mbar_init(smem_u32(&bars->k_empty[x]), 2);  // both tiles' MMAs
+      mbar_init(smem_u32(&bars->v_full[x]), 1);
+      mbar_init(smem_u32(&bars->v_empty[x]), 3);  // and the value ends' warp
       mbar_init(smem_u32(&bars->q_full[x]), 1);
       mbar_init(smem_u32(&bars->q_empty[x]), 1);
       mbar_init(smem_u32(&bars->s_full[x]), 1);
@@ -399,11 +399,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       tma_prefetch_desc(&tm_rope);
     }
     grid_dep_wait();  // the plan and the rotated queries
+    auto block_at = [&](uint32_t pos) { return smem_u32(sR + (pos % kPtRing) * kPtBlock); };
     const int nlist = *reinterpret_cast<volatile int*>(counts);
     const int units = a.H / pack;
     const long long total = (long long)nlist * units;
     const long long group = (long long)nlist * unit_group;
-    uint32_t use = 0, tiles[2] = {0, 0};  // ring blocks and query tiles loaded so far
+    uint32_t t = 0, tiles[2] = {0, 0};  // steps (key and value tiles) and query tiles loaded so far
     bool ok = true;
     int w = 0;
     if (lane == 0) w = atomicAdd(counts + 1, 1);
@@ -444,33 +445,27 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       auto page_id = [&](int j) {
         return lane < 2 && 2 * j + lane < np ? __ldg(page_table + (size_t)it.b * a.maxp + 2 * j + lane) : 0;
       };
-      auto acquire = [&](uint32_t bytes) {  // the next ring block
-        const uint32_t k = use % kPtRing;
-        if (use >= (uint32_t)kPtRing)
-          ok = mbar_wait_warp(smem_u32(&bars->empty[k]), (use / kPtRing - 1) & 1, abort_flag, err, kPsRing);
-        if (ok && lane == 0) mbar_expect_tx(smem_u32(&bars->full[k]), bytes);
-        __syncwarp();
-        return k;
-      };
       int id = page_id(0);
-      for (int j = 0; ok && j < n; ++j) {
+      for (int j = 0; ok && j < n; ++j, ++t) {
         const int id_next = j + 1 < n ? page_id(j + 1) : 0;
         const int pages = min(2, np - 2 * j);
-        for (int blk = 0; ok && blk < 3; ++blk) {
-          const uint32_t k = acquire(blk < 2 ? kPtBlock : pages * (kPtBlock / 2));
-          if (!ok) break;
-          const uint32_t dst = smem_u32(sR + k * kPtBlock), fb = smem_u32(&bars->full[k]);
-          if (blk < 2) {
-            if (lane == 0) tma_load_3d(dst, &tm_k, fb, 64 * blk, it.kvh, it.k0 + 128 * j);
-          } else if (lane < pages) {
+        // Keys: blocks 5 t .. 5 t + 2 of the ring, where the last of the keys and the values of step t - 2 were.
+        if (t >= 2) ok = mbar_wait_warp(smem_u32(&bars->v_empty[t & 1]), ((t >> 1) - 1) & 1, abort_flag, err, kPsRing);
+        if (!ok) break;
+        {
+          const uint32_t fb = smem_u32(&bars->k_full[t & 1]);
+          if (lane == 0) mbar_expect_tx(fb, 2 * kPtBlock + pages * (kPtBlock / 2));
+          __syncwarp();
+          if (lane < pages) {  // the rotary keys, a page a lane
             if (id < 0 || id >= a.num_pages) {  // reported, and read from page 0 instead
               report_error(err, kErrDeviceCheck, it.b, (2 * j + lane) * kPage);
               id = 0;
             }
-            tma_load_2d(dst + lane * (kPtBlock / 2), &tm_rope, fb, 0, id * kPage);
+            tma_load_2d(block_at(5 * t + 2) + lane * (kPtBlock / 2), &tm_rope, fb, 0, id * kPage);
+          } else if (lane >= 2 && lane < 4) {
+            tma_load_3d(block_at(5 * t + lane - 2), &tm_k, fb, 64 * (lane - 2), it.kvh, it.k0 + 128 * j);
           }
           __syncwarp();
-          ++use;
         }
         if (j == 0) {  // the query tiles, once the last QK^T of the item before has read theirs
           for (int x = 0; ok && x < 2; ++x) {
@@ -480,32 +475,39 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (!ok) break;
             if (lane == 0) {
               const uint32_t fb = smem_u32(&bars->q_full[x]), dst = smem_u32(sQ + 3 * x * kPtBlock);
-              const int t = it.q0 + it.tok0 + x * TT;
+              const int tok = it.q0 + it.tok0 + x * TT;
               mbar_expect_tx(fb, 3 * kPtBlock);
-              tma_load_3d(dst, &tm_qn, fb, 0, it.head0, t);
-              tma_load_3d(dst + kPtBlock, &tm_qn, fb, 64, it.head0, t);
-              tma_load_3d(dst + 2 * kPtBlock, &tm_qr, fb, 0, it.head0, t);
+              tma_load_3d(dst, &tm_qn, fb, 0, it.head0, tok);
+              tma_load_3d(dst + kPtBlock, &tm_qn, fb, 64, it.head0, tok);
+              tma_load_3d(dst + 2 * kPtBlock, &tm_qr, fb, 0, it.head0, tok);
             }
             __syncwarp();
             ++tiles[x];
           }
-        }
-        for (int half = 0; ok && half < 2; ++half) {  // 64 tokens of V
-          const uint32_t k = acquire(kPtBlock);
           if (!ok) break;
-          if (lane < 2)
-            tma_load_3d(smem_u32(sR + k * kPtBlock + lane * (kPtBlock / 2)), &tm_v, smem_u32(&bars->full[k]), 64 * lane,
-                        it.kvh, it.k0 + 128 * j + 64 * half);
+        }
+        // Values: blocks 5 t + 3, 5 t + 4, where the first two of the keys of step t - 1 were.
+        if (t >= 1)
+          ok = mbar_wait_warp(smem_u32(&bars->k_empty[(t - 1) & 1]), ((t - 1) >> 1) & 1, abort_flag, err, kPsRing);
+        if (!ok) break;
+        {
+          const uint32_t fb = smem_u32(&bars->v_full[t & 1]);
+          if (lane == 0) mbar_expect_tx(fb, 2 * kPtBlock);
           __syncwarp();
-          ++use;
+          if (lane < 4)  // 64 tokens x 64 dims a lane
+            tma_load_3d(block_at(5 * t + 3 + (lane >> 1)) + (lane & 1) * (kPtBlock / 2), &tm_v, fb, 64 * (lane & 1),
+                        it.kvh, it.k0 + 128 * j + 64 * (lane >> 1));
+          __syncwarp();
         }
         id = id_next;
       }
       w = __shfl_sync(0xffffffffu, w_next, 0);
     }
-    if (*abort_flag) {
-      for (uint32_t u = use > (uint32_t)kPtRing ? use - kPtRing : 0; u < use; ++u)
-        drain_wait(smem_u32(&bars->full[u % kPtRing]), (u / kPtRing) & 1);
+    if (*abort_flag) {  // what may still be on its way: the last two steps and the step that was broken off
+      for (uint32_t u = t > 1 ? t - 2 : 0; u <= t; ++u) {
+        if (u < t || !ok) drain_wait(smem_u32(&bars->k_full[u & 1]), (u >> 1) & 1);
+        if (u < t) drain_wait(smem_u32(&bars->v_full[u & 1]), (u >> 1) & 1);
+      }
       for (int x = 0; x < 2; ++x)
         if (tiles[x] > 0) drain_wait(smem_u32(&bars->q_full[x]), (tiles[x] - 1) & 1);
     }
@@ -517,15 +519,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     // other's products.
     if (elect_one()) {
       const int x = warp >> 1;
-      uint32_t base = 0;               // ring position of the item's first block
+      uint32_t t0 = 0;                 // steps of the items before
       uint32_t tiles = 0, steps = 0;   // query tiles begun, P buffers taken
       uint32_t ends = 0, turns = 0;    // value tiles with an end, turns taken
       const uint64_t qd0 = sdesc_sw128(smem_u32(sQ + 3 * x * kPtBlock), 16, 1024);
       const uint64_t kd0 = sdesc_sw128(smem_u32(sR), 16, 1024), vd0 = sdesc_sw128(smem_u32(sR), kPtBlock / 2, 1024);
       const uint32_t s_col = tmem + 128u * x, o_col = tmem + kPtColO + 128u * x;
       bool ok = true, owed = false;
-      auto wait_block = [&](uint32_t pos) {
-        ok = ok && mbar_wait(smem_u32(&bars->full[pos % kPtRing]), (pos / kPtRing) & 1, abort_flag, err, kPsK);
+      auto wait_keys = [&](uint32_t t) {
+        ok = ok && mbar_wait(smem_u32(&bars->k_full[t & 1]), (t >> 1) & 1, abort_flag, err, kPsK);
+      };
+      auto wait_values = [&](uint32_t t) {
+        ok = ok && mbar_wait(smem_u32(&bars->v_full[t & 1]), (t >> 1) & 1, abort_flag, err, kPsV);
       };
       auto block = [&](uint32_t pos) { return (uint64_t)((pos % kPtRing) * (kPtBlock >> 4)); };
       for (uint32_t i = 0; ok; ++i) {
@@ -536,49 +541,42 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         mbar_arrive(smem_u32(&bars->item_empty[sl]));
         if (!live) break;
         const int mine = x ? n1 : n0, n = max(n0, n1);
-        auto wait_keys = [&](int j) {
-#pragma unroll
-          for (int blk = 0; blk < 3; ++blk) wait_block(base + 5u * j + blk);
-        };
         auto qk = [&](int j) {
-          const uint32_t kp = base + 5u * j;
+          const uint32_t t = t0 + j;
 #pragma unroll
           for (int blk = 0; blk < 3; ++blk)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_ss(s_col, qd0 + (uint64_t)(blk * (kPtBlock >> 4) + 2 * ks), kd0 + block(kp + blk) + (uint64_t)(2 * ks),
+              mma_ss(s_col, qd0 + (uint64_t)(blk * (kPtBlock >> 4) + 2 * ks), kd0 + block(5 * t + blk) + (uint64_t)(2 * ks),
                      kIdescQK, (blk | ks) ? 1u : 0u);
           mma_commit(smem_u32(&bars->s_full[x]));
-#pragma unroll
-          for (int blk = 0; blk < 3; ++blk) mma_commit(smem_u32(&bars->empty[(kp + blk) % kPtRing]));
+          mma_commit(smem_u32(&bars->k_empty[t & 1]));
           if (j + 1 == mine) mma_commit(smem_u32(&bars->q_empty[x]));
         };
         auto pv = [&](int j) {
-          const uint32_t vp = base + 5u * j + 3u;
+          const uint32_t t = t0 + j;
 #pragma unroll
           for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_ts(o_col, s_col + 32u * half + 8u * ks, vd0 + block(vp + half) + (uint64_t)((ks * 2048) >> 4), kIdescPV,
+              mma_ts(o_col, s_col + 32u * half + 8u * ks, vd0 + block(5 * t + 3 + half) + (uint64_t)((ks * 2048) >> 4),
+                     kIdescPV,
                      (j | half | ks) ? 1u : 0u);
-          mma_commit(smem_u32(&bars->empty[vp % kPtRing]));
-          mma_commit(smem_u32(&bars->empty[(vp + 1) % kPtRing]));
+          mma_commit(smem_u32(&bars->v_empty[t & 1]));
           if (j + 1 == mine) mma_commit(smem_u32(&bars->o_full[x]));
         };
         if (mine > 0) {
           ok = mbar_wait(smem_u32(&bars->q_full[x]), tiles & 1, abort_flag, err, kPsQ);
           ++tiles;
-          wait_keys(0);
+          wait_keys(t0);
           if (ok) {
             tc_fence_after();
             qk(0);
           }
           for (int j = 0; ok && j < mine; ++j, ++steps) {
             // everything that the step needs, so that no wait stands between its MMAs; P comes last
-            const uint32_t vp = base + 5u * j + 3u;
-            wait_block(vp);
-            wait_block(vp + 1);
-            if (j + 1 < mine) wait_keys(j + 1);
+            wait_values(t0 + j);
+            if (j + 1 < mine) wait_keys(t0 + j + 1);
             if (Lk < 128 * (j + 1))
               ok = ok && mbar_wait(smem_u32(&bars->v_fixed[ends & 1]), (ends >> 1) & 1, abort_flag, err, kPsV);
             if (j == 0 && tiles > 1)  // the item before has read its O
@@ -594,12 +592,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (owed) mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
           }
         }
-        // blocks that only the other tile reads: passed on as they come
-        for (uint32_t pos = base + 5u * mine; ok && pos < base + 5u * n; ++pos) {
-          wait_block(pos);
-          if (ok) mbar_arrive(smem_u32(&bars->empty[pos % kPtRing]));
+        // steps that only the other tile takes: passed on as they come
+        for (uint32_t t = t0 + mine; ok && t < t0 + n; ++t) {
+          wait_keys(t);
+          if (ok) mbar_arrive(smem_u32(&bars->k_empty[t & 1]));
+          wait_values(t);
+          if (ok) mbar_arrive(smem_u32(&bars->v_empty[t & 1]));
         }
-        base += 5u * n;
+        t0 += n;
         ends += n > 0 && Lk < 128 * n;
       }
       if (*abort_flag) {
@@ -610,35 +610,31 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------ value rows past a sequence's end
-    // Follows the ring block by block; a value block with an end is zeroed behind it.
-    uint32_t pos = 0, ends = 0;
+    uint32_t t = 0, ends = 0;
     bool ok = true;
     PromptItem it;
     for (uint32_t i = 0; ok && take(i, &it) && it.live; ++i) {
       const int n = max(it.n[0], it.n[1]);
-      for (int j = 0; ok && j < n; ++j) {
+      for (int j = 0; ok && j < n; ++j, ++t) {
         const int rows = it.Lk - 128 * j;  // of the value tile, inside the sequence
-        for (int blk = 0; ok && blk < 5; ++blk, ++pos) {
-          const uint32_t k = pos % kPtRing;
-          ok = mbar_wait_warp(smem_u32(&bars->full[k]), (pos / kPtRing) & 1, abort_flag, err, kPsV);
-          if (!ok) break;
-          const int have = rows - 64 * (blk - 3);
-          if (blk >= 3 && have < 64) {
-            const int r0 = max(0, have), nz = (64 - r0) * 8;  // 16-byte pieces of each half of the dims
-            uint8_t* to = sR + k * kPtBlock + r0 * 128;
+        ok = mbar_wait_warp(smem_u32(&bars->v_full[t & 1]), (t >> 1) & 1, abort_flag, err, kPsV);
+        if (!ok) break;
+        if (rows < 128) {  // the sequence's last value tile
+          for (int half = 0; half < 2; ++half) {
+            const int r0 = min(64, max(0, rows - 64 * half)), nz = (64 - r0) * 8;  // 16-byte pieces of 64 dims
+            uint8_t* to = sR + ((5 * t + 3 + half) % kPtRing) * kPtBlock + r0 * 128;
             for (int e = lane; e < nz; e += 32)
 #pragma unroll
               for (int d = 0; d < 2; ++d)
                 *reinterpret_cast<uint4*>(to + d * (kPtBlock / 2) + e * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
           }
+          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->empty[k]));
-        }
-        if (ok && rows < 128) {  // the sequence's last value tile
           if (lane == 0) mbar_arrive(smem_u32(&bars->v_fixed[ends & 1]));
           ++ends;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->v_empty[t & 1]));
       }
     }
   }
