@@ -30,7 +30,10 @@
 //     finds the step's own, with P held back in registers; only when a row's
 //     maximum has grown by more than 2^8 the scores are read again and O, which
 //     the same thread owns, is rescaled: the scores of step j being there
-//     implies that PV of step j - 1 is done.
+//     implies that PV of step j - 1 is done.  Masks, the first step's maximum and
+//     the rescaling are short loops over TMEM beside the one unrolled body, for
+//     instructions that are met once an item come from far away (unrolled, a
+//     masked step took 3600 cycles more, now 600).
 //   * Value rows past a sequence's end are zeroed in shared memory before the
 //     product (a NaN there would get past P = 0); key rows past it are masked.
 //   * The rotation of the queries runs in the kernel before this one, beside
@@ -39,8 +42,6 @@
 //   * Every wait is bounded; a CTA that gives up records the site, lets its
 //     copies and MMAs in flight end and leaves.
 #include <cuda.h>
-
-#include <type_traits>
 
 #include "host_cache.h"
 #include "launch.h"
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_col = tmem + lane_off + 128u * x, o_col = tmem + lane_off + kPtColO + 128u * x;
     const float sc = a.scale_log2, jump = kPtRescale / sc;
+    const bool wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
     uint32_t steps = 0, tiles = 0;
     bool ok = true;
     PromptItem it;
@@ -261,43 +263,53 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const int lim = min(it.Lk - it.Lq + tok, it.Lk - 1);  // the row's last key
       const size_t at = (size_t)(it.q0 + tok) * a.H + head;
       float m = -INFINITY, l = 0.f;
+      auto largest = [&](float t, const uint32_t (&v)[32]) {
+        float t0 = t, t1 = __uint_as_float(v[0]);
+#pragma unroll
+        for (int c = 1; c < 31; c += 3) {
+          t0 = fmaxf(fmaxf(t0, __uint_as_float(v[c])), __uint_as_float(v[c + 1]));
+          t1 = fmaxf(t1, __uint_as_float(v[c + 2]));
+        }
+        return fmaxf(fmaxf(t0, t1), __uint_as_float(v[31]));
+      };
       for (int j = 0; j < n; ++j, ++steps) {
         ok = mbar_wait_warp(smem_u32(&bars->s_full[x]), steps & 1, abort_flag, err, kPsS);
         if (!ok) break;
         tc_fence_after();
         const int cmax = lim - 128 * j;
-        const bool masked = __any_sync(0xffffffffu, cmax < 127);
-        // scores c0 .. c0 + 63 of the row, -inf past its last key
-        auto load = [&](auto ends, int c0, uint32_t (&v)[32], uint32_t (&w)[32]) {
-          tmem_ld32x2(s_col + c0, s_col + c0 + 32, v, w);
-          if constexpr (decltype(ends)::value) {
+        if (__any_sync(0xffffffffu, cmax < 127)) {  // -inf past the row's last key, in place
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(s_col + c, v);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (c0 + c > cmax) v[c] = 0xff800000u;
-              if (c0 + 32 + c > cmax) w[c] = 0xff800000u;
-            }
+            for (int u = 0; u < 16; ++u)
+              if (c + u > cmax) v[u] = 0xff800000u;
+            tmem_st16(s_col + c, v);
           }
-        };
-        auto largest = [&](float t, const uint32_t (&v)[32]) {
-          float t0 = t, t1 = __uint_as_float(v[0]);
+        }
+        if (j == 0) {  // the first step's own maximum
+          m = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(s_col + c, v);
 #pragma unroll
-          for (int c = 1; c < 31; c += 3) {
-            t0 = fmaxf(fmaxf(t0, __uint_as_float(v[c])), __uint_as_float(v[c + 1]));
-            t1 = fmaxf(t1, __uint_as_float(v[c + 2]));
+            for (int u = 0; u < 16; u += 2) m = fmaxf(fmaxf(m, __uint_as_float(v[u])), __uint_as_float(v[u + 1]));
           }
-          return fmaxf(fmaxf(t0, t1), __uint_as_float(v[31]));
-        };
+        }
         uint32_t p[4][16];  // P of 32 keys each, packed
-        float top, sum;
-        auto exponentials = [&](auto ends) {
+        float sum;
+        while (true) {
+          // against the maximum so far; the scores stay where they are until it is known that this will do
           const float ref = m == -INFINITY ? 0.f : -m * sc;  // no key so far: every term is 2^-inf = 0
           const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(ref, ref);
           float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          top = -INFINITY;
+          float top = -INFINITY;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t v[2][32];
-            load(ends, 64 * h, v[0], v[1]);
+            tmem_ld32x2(s_col + 64 * h, s_col + 64 * h + 32, v[0], v[1]);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               top = largest(top, v[g]);
@@ -313,30 +325,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
           }
           sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-        };
-        if (j == 0) {
-          m = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[32], w[32];
-            load(std::true_type(), 64 * h, v, w);
-            m = largest(largest(m, v), w);
-          }
-        }
-        // against the maximum so far; the scores stay where they are until it is known that this will do
-        if (masked)
-          exponentials(std::true_type());
-        else
-          exponentials(std::false_type());
-        if (j > 0 && __any_sync(0xffffffffu, top > m + jump)) {
+          if (!__any_sync(0xffffffffu, top > m + jump)) break;
+          // a row's maximum has grown by more than 2^8: rescale what there is, and once more
           float corr = 1.f;
           if (top > m + jump) {
             corr = ex2((m - top) * sc);
             m = top;
           }
           l *= corr;
-          exponentials(std::true_type());
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 128; c += 16) {
             uint32_t o[16];
             tmem_ld16(o_col + c, o);
@@ -360,30 +357,32 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (!ok) break;
         tc_fence_after();
       }
+      // O out of TMEM first, so that the next item's PV may go ahead, then the row in 32-byte pieces
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      __nv_bfloat16* dst = out + at * 128;
+      uint32_t pk[64];
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
-        if (n > 0) tmem_ld32(o_col + c, o);
-        if (mine) {
+        if (n > 0) tmem_ld32(o_col + 32 * c, o);
 #pragma unroll
-          for (int u = 0; u < 32; u += 8) {
-            uint4 pk = make_uint4(0, 0, 0, 0);
-            if (l != 0.f) {
-              pk.x = pack_bf16x2(__uint_as_float(o[u]) * inv, __uint_as_float(o[u + 1]) * inv);
-              pk.y = pack_bf16x2(__uint_as_float(o[u + 2]) * inv, __uint_as_float(o[u + 3]) * inv);
-              pk.z = pack_bf16x2(__uint_as_float(o[u + 4]) * inv, __uint_as_float(o[u + 5]) * inv);
-              pk.w = pack_bf16x2(__uint_as_float(o[u + 6]) * inv, __uint_as_float(o[u + 7]) * inv);
-            }
-            *reinterpret_cast<uint4*>(dst + c + u) = pk;
-          }
-        }
+        for (int u = 0; u < 16; ++u)
+          pk[16 * c + u] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv);
       }
       if (n > 0) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->o_free[x]));
+      }
+      if (mine) {
+        __nv_bfloat16* dst = out + at * 128;
+        if (wide) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 8) st_global_32(dst + 2 * c, pk + c);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; c += 4)
+            *reinterpret_cast<uint4*>(dst + 2 * c) = make_uint4(pk[c], pk[c + 1], pk[c + 2], pk[c + 3]);
+        }
       }
       if (lse && mine) lse[at] = l == 0.f ? -INFINITY : m * sc + log2f(l);
     }
@@ -406,31 +405,57 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const long long group = (long long)nlist * unit_group;
     uint32_t t = 0, tiles[2] = {0, 0};  // steps (key and value tiles) and query tiles loaded so far
     bool ok = true;
+    auto unit_of = [&](long long w, int2* entry) {  // the item's heads, and where its tiles are listed
+      const int g = (int)(w / group), r = (int)(w - g * group);
+      const int nu = min(unit_group, units - g * unit_group);  // units of this group
+      *entry = __ldcg(list + r / nu);
+      return g * unit_group + r % nu;
+    };
+    auto decode = [&](int unit, int2 e) {
+      const PromptSeq s = prompt_seq(cu_q, cu_k, e.x, a, nullptr);
+      PromptItem it;
+      it.live = 1;
+      it.b = e.x;
+      it.head0 = unit * pack;
+      it.kvh = it.head0 / (a.H / a.kv_heads);
+      it.tok0 = 2 * e.y * TT;
+      it.Lq = s.Lq;
+      it.Lk = s.Lk;
+      it.q0 = s.q0;
+      it.k0 = s.k0;
+      it.n[0] = key_tiles(s, it.tok0, TT);
+      it.n[1] = key_tiles(s, it.tok0 + TT, TT);
+      return it;
+    };
+    // an item's query tiles and first steps towards L2, a box per lane
+    auto fetch = [&](const PromptItem& it) {
+      if (lane < 6) {
+        const int x = lane / 3, blk = lane % 3, tok = it.q0 + it.tok0 + x * TT;
+        if (it.n[x] > 0) tma_prefetch_l2_3d(blk < 2 ? &tm_qn : &tm_qr, 64 * (blk & 1), it.head0, tok);
+      } else if (lane >= 8 && lane < 20) {
+        const int e = lane - 8, j = e / 6, blk = e % 6;  // step j: two key boxes, four value boxes
+        if (j < max(it.n[0], it.n[1])) {
+          if (blk < 2)
+            tma_prefetch_l2_3d(&tm_k, 64 * blk, it.kvh, it.k0 + 128 * j);
+          else
+            tma_prefetch_l2_3d(&tm_v, 64 * (blk & 1), it.kvh, it.k0 + 128 * j + 64 * ((blk - 2) >> 1));
+        }
+      }
+      __syncwarp();
+    };
     int w = 0;
     if (lane == 0) w = atomicAdd(counts + 1, 1);
     w = __shfl_sync(0xffffffffu, w, 0);
+    PromptItem it;
+    it.live = 0;
+    if (w < total) {
+      int2 e;
+      const int unit = unit_of(w, &e);
+      it = decode(unit, e);
+    }
     for (uint32_t i = 0; ok; ++i) {
       int w_next = 0;
-      if (lane == 0 && w < total) w_next = atomicAdd(counts + 1, 1);  // not needed before the next turn
-      PromptItem it;
-      it.live = w < total;
-      if (it.live) {
-        const int g = (int)(w / group), r = (int)(w - g * group);
-        const int nu = min(unit_group, units - g * unit_group);  // units of this group
-        const int2 e = __ldcg(list + r / nu);
-        const int unit = g * unit_group + r % nu;
-        const PromptSeq s = prompt_seq(cu_q, cu_k, e.x, a, nullptr);
-        it.b = e.x;
-        it.head0 = unit * pack;
-        it.kvh = it.head0 / (a.H / a.kv_heads);
-        it.tok0 = 2 * e.y * TT;
-        it.Lq = s.Lq;
-        it.Lk = s.Lk;
-        it.q0 = s.q0;
-        it.k0 = s.k0;
-        it.n[0] = key_tiles(s, it.tok0, TT);
-        it.n[1] = key_tiles(s, it.tok0 + TT, TT);
-      }
+      if (lane == 0 && it.live) w_next = atomicAdd(counts + 1, 1);  // looked at from the second step on
       const int sl = i & 1;
       if (i >= 2 && !mbar_wait_warp(smem_u32(&bars->item_empty[sl]), ((i >> 1) - 1) & 1, abort_flag, err, kPsItemFree))
         break;
@@ -445,8 +470,27 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       auto page_id = [&](int j) {
         return lane < 2 && 2 * j + lane < np ? __ldg(page_table + (size_t)it.b * a.maxp + 2 * j + lane) : 0;
       };
+      // The next item is looked up a bit at a time between this one's loads.
+      PromptItem nxt;
+      nxt.live = 0;
+      int looked = 0, unit = 0;
+      int2 entry;
+      auto look_ahead = [&] {
+        if (looked == 0) {
+          w = __shfl_sync(0xffffffffu, w_next, 0);
+          if (w < total)
+            unit = unit_of(w, &entry);
+          else
+            looked = 1;
+        } else if (w < total) {
+          nxt = decode(unit, entry);
+          fetch(nxt);
+        }
+        ++looked;
+      };
       int id = page_id(0);
       for (int j = 0; ok && j < n; ++j, ++t) {
+        if (j > 0 && looked < 2) look_ahead();
         const int id_next = j + 1 < n ? page_id(j + 1) : 0;
         const int pages = min(2, np - 2 * j);
         // Keys: blocks 5 t .. 5 t + 2 of the ring, where the last of the keys and the values of step t - 2 were.
@@ -501,7 +545,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         id = id_next;
       }
-      w = __shfl_sync(0xffffffffu, w_next, 0);
+      while (looked < 2) look_ahead();
+      it = nxt;
     }
     if (*abort_flag) {  // what may still be on its way: the last two steps and the step that was broken off
       for (uint32_t u = t > 1 ? t - 2 : 0; u <= t; ++u) {
@@ -543,12 +588,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int mine = x ? n1 : n0, n = max(n0, n1);
         auto qk = [&](int j) {
           const uint32_t t = t0 + j;
+          wait_keys(t);
+          if (!ok) return;
+          tc_fence_after();
 #pragma unroll
-          for (int blk = 0; blk < 3; ++blk)
+          for (int blk = 0; blk < 3; ++blk) {
+            // the other tile's turn: it is here by the time that the rest has gone into the pipe
+            if (blk == 2 && owed) mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               mma_ss(s_col, qd0 + (uint64_t)(blk * (kPtBlock >> 4) + 2 * ks), kd0 + block(5 * t + blk) + (uint64_t)(2 * ks),
                      kIdescQK, (blk | ks) ? 1u : 0u);
+          }
           mma_commit(smem_u32(&bars->s_full[x]));
           mma_commit(smem_u32(&bars->k_empty[t & 1]));
           if (j + 1 == mine) mma_commit(smem_u32(&bars->q_empty[x]));
@@ -568,28 +619,27 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (mine > 0) {
           ok = mbar_wait(smem_u32(&bars->q_full[x]), tiles & 1, abort_flag, err, kPsQ);
           ++tiles;
-          wait_keys(t0);
-          if (ok) {
-            tc_fence_after();
-            qk(0);
-          }
+          const bool waits = owed;
+          owed = false;
+          qk(0);
+          owed = waits;
           for (int j = 0; ok && j < mine; ++j, ++steps) {
-            // everything that the step needs, so that no wait stands between its MMAs; P comes last
             wait_values(t0 + j);
-            if (j + 1 < mine) wait_keys(t0 + j + 1);
             if (Lk < 128 * (j + 1))
               ok = ok && mbar_wait(smem_u32(&bars->v_fixed[ends & 1]), (ends >> 1) & 1, abort_flag, err, kPsV);
             if (j == 0 && tiles > 1)  // the item before has read its O
               ok = ok && mbar_wait(smem_u32(&bars->o_free[x]), (tiles - 2) & 1, abort_flag, err, kPsOFree);
             if (x ? j < n0 : owed)  // strictly in turn: no token is passed before the last one was taken
               ok = ok && mbar_wait(smem_u32(&bars->turn[x]), turns++ & 1, abort_flag, err, kPsTurn);
-            ok = ok && mbar_wait(smem_u32(&bars->p_full[x]), steps & 1, abort_flag, err, kPsP);
+            ok = ok && mbar_poll(smem_u32(&bars->p_full[x]), steps & 1, abort_flag, err, kPsP);
             if (!ok) break;
             tc_fence_after();
             pv(j);
-            if (j + 1 < mine) qk(j + 1);
-            owed = j < (x ? n0 : n1);  // the other tile has this step too
-            if (owed) mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
+            owed = j < (x ? n0 : n1);  // the other tile has this step too, and waits for its turn
+            if (j + 1 < mine)
+              qk(j + 1);  // its keys may land while PV runs
+            else if (owed)
+              mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
           }
         }
         // steps that only the other tile takes: passed on as they come
