@@ -266,44 +266,70 @@ def latent_append_noalloc(dims, d_model, h, W_DKV, W_KR, pos, page_table, latent
                                        _stream(stream)))
 
 
-class _Args:
-    """The tensors of one call: checked for shape, type, layout and a common
-    device before anything is enqueued, then passed on that device."""
+_TYPES = None  # torch's types by the dims' dtype number, and for "i32" and "f32"
 
-    def __init__(self, dims: Dims):
-        self.device = None
-        self.dtype = {v: k for k, v in DTYPES.items()}[dims.dtype]
 
-    def __call__(self, name, x, shape, dtype, strided=False):
+def _types():
+    global _TYPES
+    if _TYPES is None:
         import torch
-        want = {"f32": torch.float32, "bf16": torch.bfloat16, "i32": torch.int32, "bytes": torch.uint8}[dtype]
-        if not isinstance(x, torch.Tensor) or not x.is_cuda:
-            raise MlraError(1, f"{name} has to be a CUDA tensor")
-        if self.device is None:
-            self.device = x.device
-        if x.device != self.device:
-            raise MlraError(1, f"{name} is on {x.device}, others on {self.device}")
-        if x.dtype != want and dtype != "bytes":
-            raise MlraError(1, f"{name} is {x.dtype}, not {want}")
-        if shape is not None and tuple(x.shape) != tuple(shape):
-            raise MlraError(1, f"{name} has shape {tuple(x.shape)}, not {tuple(shape)}")
-        if not (x.stride(-1) == 1 or x.shape[-1] == 1 or x.numel() == 0) if strided else not x.is_contiguous():
-            raise MlraError(1, f"{name} has to be contiguous" + (" in its last axis" if strided else ""))
-        return x.data_ptr() or None
+        _TYPES = {DTYPES["f32"]: torch.float32, DTYPES["bf16"]: torch.bfloat16, "f32": torch.float32,
+                  "i32": torch.int32}
+    return _TYPES
 
-    def workspace(self, x):
-        return self("workspace", x, None, "bytes"), x.numel() * x.element_size()
 
-    def run(self, fn, stream, *args):
-        import torch
-        with torch.cuda.device(self.device):
-            _check(fn(*args, _stream(stream)))
+def _refuse(name, x, shape, dtype, strided, device):
+    """The reason why a tensor of a call is refused."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        why = "has to be a CUDA tensor"
+    elif device is not None and x.get_device() != device:
+        why = f"is on {x.device}, others on cuda:{device}"
+    elif x.dtype is not dtype:
+        why = f"is {x.dtype}, not {dtype}"
+    elif tuple(x.shape) != shape:
+        why = f"has shape {tuple(x.shape)}, not {shape}"
+    else:
+        why = "has to be contiguous" + (" in its last axis" if strided else "")
+    raise MlraError(1, f"{name} {why}")
+
+
+def _run(fn, dims, stream, workspace, tensors, lead=(), strided=()):
+    """Calls ``fn`` with ``dims``, the addresses of ``tensors`` ((name, tensor, shape, type), checked for shape, type,
+    layout and a common device before anything is enqueued) and the workspace, on the tensors' device.  An entry
+    whose tensor is None passes NULL."""
+    import torch
+    device, args = None, []
+    for name, x, shape, dtype in tensors:
+        if x is None:
+            args.append(None)
+            continue
+        try:
+            ok = x.dtype is dtype and x.shape == shape and x.is_cuda and \
+                (x.is_contiguous() or (name in strided and (x.stride(-1) == 1 or x.shape[-1] == 1 or x.numel() == 0)))
+        except AttributeError:
+            ok = False
+        if not ok or (device is not None and x.get_device() != device):
+            _refuse(name, x, shape, dtype, name in strided, device)
+        if device is None:
+            device = x.get_device()
+        args.append(x.data_ptr() or None)
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != device or not workspace.is_contiguous():
+        raise MlraError(1, f"workspace has to be a contiguous tensor on cuda:{device}")
+    args += (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if device == torch.cuda.current_device():
+        status = fn(ctypes.byref(dims), *lead, *args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            status = fn(ctypes.byref(dims), *lead, *args, _stream(stream))
+    if status != MLRA_OK:
+        raise MlraError(status, last_error())
 
 
 def _prompt_shape(q_nope, q_rope, k_nope, v) -> PromptShape:
     s = PromptShape(k_nope.shape[1], q_nope.shape[0], k_nope.shape[0])
-    for name, x in (("q_nope_stride", q_nope), ("q_rope_stride", q_rope), ("k_nope_stride", k_nope), ("v_stride", v)):
-        getattr(s, name)[:] = x.stride()[:2]
+    for field, x in ((s.q_nope_stride, q_nope), (s.q_rope_stride, q_rope), (s.k_nope_stride, k_nope), (s.v_stride, v)):
+        field[0], field[1], _ = x.stride()
     return s
 
 
@@ -323,48 +349,43 @@ def mla_prompt(dims, q_nope, q_rope, cu_q, k_nope, v, cu_k, rope_cache, page_tab
                stream=None):
     """Causal attention of packed prompts into out [total_q,H,d_v] (see include/mlra_serving.h); q_nope, q_rope,
     k_nope and v may be strided views, k_nope.shape[1] is the number of kv heads."""
-    d, a = dims, _Args(dims)
-    for name, x in (("q_nope", q_nope), ("k_nope", k_nope)):
+    for name, x in (("q_nope", q_nope), ("q_rope", q_rope), ("k_nope", k_nope), ("v", v)):
         if getattr(x, "ndim", 0) != 3:
             raise MlraError(1, f"{name} has to be [tokens, heads, width]")
-    T, S, kv = q_nope.shape[0], k_nope.shape[0], k_nope.shape[1]
-    args = (a("q_nope", q_nope, (T, d.H, d.d_h), a.dtype, True), a("q_rope", q_rope, (T, d.H, d.d_r), a.dtype, True),
-            a("cu_q", cu_q, (d.B + 1,), "i32"), a("k_nope", k_nope, (S, kv, d.d_h), a.dtype, True),
-            a("v", v, (S, kv, d.d_v), a.dtype, True), a("cu_k", cu_k, (d.B + 1,), "i32"),
-            a("rope_cache", rope_cache, (d.num_pages, d.page_size, d.d_r), a.dtype),
-            a("page_table", page_table, (d.B, d.max_pages_per_seq), "i32"), a("out", out, (T, d.H, d.d_v), a.dtype),
-            None if lse is None else a("lse", lse, (T, d.H), "f32"), *a.workspace(workspace))
-    if T == 0:
-        return
-    shape = _prompt_shape(q_nope, q_rope, k_nope, v)
-    a.run(lib().mla_prompt, stream, ctypes.byref(dims), ctypes.byref(shape), *args)
+    B, H, d_h, d_r, d_v = dims.B, dims.H, dims.d_h, dims.d_r, dims.d_v
+    ty, (T, S, kv) = _types(), (q_nope.shape[0], *k_nope.shape[:2])
+    e = ty[dims.dtype]
+    _run(lib().mla_prompt, dims, stream, workspace,
+         (("q_nope", q_nope, (T, H, d_h), e), ("q_rope", q_rope, (T, H, d_r), e), ("cu_q", cu_q, (B + 1,), ty["i32"]),
+          ("k_nope", k_nope, (S, kv, d_h), e), ("v", v, (S, kv, d_v), e), ("cu_k", cu_k, (B + 1,), ty["i32"]),
+          ("rope_cache", rope_cache, (dims.num_pages, dims.page_size, d_r), e),
+          ("page_table", page_table, (B, dims.max_pages_per_seq), ty["i32"]), ("out", out, (T, H, d_v), e),
+          ("lse", lse, (T, H), ty["f32"])),
+         lead=(ctypes.byref(_prompt_shape(q_nope, q_rope, k_nope, v)),),
+         strided=("q_nope", "q_rope", "k_nope", "v"))
 
 
 def absorb_query(dims, q_nope, q_rope, q_pos, W_UK, q_abs, workspace, stream=None):
     """The decode's query folded through W_UK and rotated, times scale * log2(e), into q_abs [B,H,d_c+d_r]."""
-    d, a = dims, _Args(dims)
-    args = (a("q_nope", q_nope, (d.B, d.H, d.d_h), a.dtype), a("q_rope", q_rope, (d.B, d.H, d.d_r), a.dtype),
-            a("q_pos", q_pos, (d.B,), "i32"), a("W_UK", W_UK, (d.H, d.d_h, d.d_c), a.dtype),
-            a("q_abs", q_abs, (d.B, d.H, d.d_c + d.d_r), a.dtype), *a.workspace(workspace))
-    a.run(lib().mlra_absorb, stream, ctypes.byref(dims), *args)
-
-
-def _pools(a, d, latent_cache, rope_cache):
-    return (a("latent_cache", latent_cache, (d.num_pages, d.page_size, d.d_c), a.dtype),
-            a("rope_cache", rope_cache, (d.num_pages, d.page_size, d.d_r), a.dtype))
+    B, H, d_h, d_c, d_r = dims.B, dims.H, dims.d_h, dims.d_c, dims.d_r
+    ty = _types()
+    e = ty[dims.dtype]
+    _run(lib().mlra_absorb, dims, stream, workspace,
+         (("q_nope", q_nope, (B, H, d_h), e), ("q_rope", q_rope, (B, H, d_r), e), ("q_pos", q_pos, (B,), ty["i32"]),
+          ("W_UK", W_UK, (H, d_h, d_c), e), ("q_abs", q_abs, (B, H, d_c + d_r), e)))
 
 
 def attention_weights(dims, q_abs, lse, latent_cache, rope_cache, page_table, seq_lens, weights_in, weights, workspace,
                       stream=None):
     """weights = weights_in (None: zeros) + each cached token's attention weight over all heads and branches."""
-    d, a = dims, _Args(dims)
-    slots = (d.B, d.max_pages_per_seq * d.page_size)
-    args = (a("q_abs", q_abs, (d.B, d.H, d.d_c + d.d_r), a.dtype), a("lse", lse, (d.B, d.n_branch, d.H), "f32"),
-            *_pools(a, d, latent_cache, rope_cache), a("page_table", page_table, (d.B, d.max_pages_per_seq), "i32"),
-            a("seq_lens", seq_lens, (d.B,), "i32"),
-            None if weights_in is None else a("weights_in", weights_in, slots, "f32"),
-            a("weights", weights, slots, "f32"), *a.workspace(workspace))
-    a.run(lib().mlra_attention_weights, stream, ctypes.byref(dims), *args)
+    B, H, d_c, d_r, pages = dims.B, dims.H, dims.d_c, dims.d_r, dims.max_pages_per_seq
+    ty, pool = _types(), (dims.num_pages, dims.page_size)
+    e, slots = ty[dims.dtype], (B, pages * dims.page_size)
+    _run(lib().mlra_attention_weights, dims, stream, workspace,
+         (("q_abs", q_abs, (B, H, d_c + d_r), e), ("lse", lse, (B, dims.n_branch, H), ty["f32"]),
+          ("latent_cache", latent_cache, (*pool, d_c), e), ("rope_cache", rope_cache, (*pool, d_r), e),
+          ("page_table", page_table, (B, pages), ty["i32"]), ("seq_lens", seq_lens, (B,), ty["i32"]),
+          ("weights_in", weights_in, slots, ty["f32"]), ("weights", weights, slots, ty["f32"])))
 
 
 def evict_workspace_bytes(dims: Dims) -> int:
@@ -378,14 +399,15 @@ def latent_evict(dims, recent, evict_pages, weights, page_table, seq_lens, laten
                  page_table_out, seq_lens_out, workspace, stream=None):
     """Frees evict_pages[b] pages of each sequence: the tokens with the least weight leave, but for the last
     ``recent`` (see include/mlra_serving.h)."""
-    d, a = dims, _Args(dims)
-    slots, table = (d.B, d.max_pages_per_seq * d.page_size), (d.B, d.max_pages_per_seq)
-    args = (a("evict_pages", evict_pages, (d.B,), "i32"), a("weights", weights, slots, "f32"),
-            a("page_table", page_table, table, "i32"), a("seq_lens", seq_lens, (d.B,), "i32"),
-            *_pools(a, d, latent_cache, rope_cache), a("weights_out", weights_out, slots, "f32"),
-            a("page_table_out", page_table_out, table, "i32"), a("seq_lens_out", seq_lens_out, (d.B,), "i32"),
-            *a.workspace(workspace))
-    a.run(lib().latent_evict, stream, ctypes.byref(dims), int(recent), *args)
+    B, pages = dims.B, dims.max_pages_per_seq
+    ty, pool = _types(), (dims.num_pages, dims.page_size)
+    e, i32, f32, slots = ty[dims.dtype], ty["i32"], ty["f32"], (B, pages * dims.page_size)
+    _run(lib().latent_evict, dims, stream, workspace,
+         (("evict_pages", evict_pages, (B,), i32), ("weights", weights, slots, f32),
+          ("page_table", page_table, (B, pages), i32), ("seq_lens", seq_lens, (B,), i32),
+          ("latent_cache", latent_cache, (*pool, dims.d_c), e), ("rope_cache", rope_cache, (*pool, dims.d_r), e),
+          ("weights_out", weights_out, slots, f32), ("page_table_out", page_table_out, (B, pages), i32),
+          ("seq_lens_out", seq_lens_out, (B,), i32)), lead=(int(recent),))
 
 
 def check_status(workspace, stream=None) -> None:
