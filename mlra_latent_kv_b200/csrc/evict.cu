@@ -10,11 +10,10 @@
 //
 // Two kernels.  evict_select_kernel: a cluster of 8 CTAs per sequence finds
 // the 64 n smallest (weight, slot) by a radix select over the weights' bits
-// (four 8-bit digits; the CTAs' histograms meet in distributed shared memory)
+// (three digits; the CTAs' histograms meet in distributed shared memory)
 // and writes both lists, in slot order, beside the shifted weights, table and
 // length.  It is bound by latency: a sequence's weights are read from HBM once
-// and kept in shared memory.  evict_move_kernel: a warp per token row copies
-// the latent and the rope key, 16 bytes a lane, several rows in flight.
+// and kept in shared memory.  evict_move_kernel copies the rows, bound by HBM.
 #include <cooperative_groups.h>
 
 #include "host_cache.h"
@@ -37,13 +36,19 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+constexpr int kBins = 2048;        // of a digit: 11, 11 and 10 bits
+constexpr int kSlice = kBins / kCluster;  // bins that a CTA adds up for the cluster
+constexpr int kAlone = 4096;       // a sequence that one CTA takes alone, without the cluster's barriers
+static_assert(kSlice % 32 == 0 && kSlice <= kSelThreads, "a thread per bin of a slice");
+
 struct SelShared {
-  int hist[2][256];            // of this CTA, double-buffered over the digits
-  int total[256];              // over the cluster
+  int hist[2][kBins];          // of this CTA, double-buffered over the digits
+  int warp_sum[kSelWarps];
   int ties[kSelWarps];         // equal to the threshold, per warp
   int srcs[kSelWarps];         // tokens to move, per warp
   int holes[kSelWarps];        // slots to move to, per warp
-  int digit, below;
+  int slice[kCluster];         // keys in each CTA's slice of the bins
+  int found[3];                // the digit, the keys below it, the keys that have it
 };
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
@@ -52,7 +57,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
                         float* __restrict__ weights_out, int* __restrict__ page_table_out,
                         int* __restrict__ seq_lens_out, int* __restrict__ err, EvictWorkspace ws, EvictArgs a) {
   extern __shared__ uint32_t keys[];
-  __shared__ SelShared sh;
+  __shared__ __align__(16) SelShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int b = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -69,7 +74,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
   const int C = n > 0 ? L - a.recent : 0;  // tokens that may leave: slots [0, C)
 
   // this CTA's slots, and within them each warp's
-  const int per = (L + kCluster - 1) / kCluster;
+  const bool alone = L <= kAlone;
+  const int ctas = alone ? 1 : kCluster;
+  auto meet = [&] {  // all CTAs that share the sequence
+    if (alone)
+      __syncthreads();
+    else
+      cluster.sync();
+  };
+  const int per = (L + ctas - 1) / ctas;
   const int lo = min(L, rank * per), hi = min(L, lo + per);
   const bool in_smem = per <= kKeyCap;
   const int wper = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
@@ -78,67 +91,85 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
 
   uint32_t T = 0;  // the largest key that leaves
   int spare = 0;   // of the tokens with that key, in slot order, the first `spare` stay
-  if (E > 0) {     // uniform over the cluster
+  if (E > 0 && rank < ctas) {  // uniform over the CTAs that meet
     if (in_smem)
       for (int t = lo + threadIdx.x; t < hi; t += kSelThreads) keys[t - lo] = order_key(__ldg(w + t));
-    for (int i = threadIdx.x; i < 512; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+    for (int i = threadIdx.x; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
     __syncthreads();
     int need = E;  // how many of the keys that share the digits found so far leave
-    for (int d = 0; d < 4; ++d) {
-      const int shift = 24 - 8 * d;
-      const uint32_t mask = d == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    for (int d = 0; d < 3; ++d) {
+      const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+      const uint32_t digits = d == 2 ? 1023u : 2047u, mask = d == 0 ? 0u : 0xFFFFFFFFu << (d == 1 ? 21 : 10);
       int* hist = sh.hist[d & 1];
       for (int t = lo + threadIdx.x; t < min(hi, C); t += kSelThreads) {
         const uint32_t u = key_at(t);
-        if ((u & mask) == T) atomicAdd(&hist[(u >> shift) & 255], 1);
+        if ((u & mask) == T) atomicAdd(&hist[(u >> shift) & digits], 1);
       }
-      cluster.sync();
-      if (threadIdx.x < 256) {
-        int s = 0;
-#pragma unroll
-        for (int r = 0; r < kCluster; ++r) s += cluster.map_shared_rank(hist, r)[threadIdx.x];
-        sh.total[threadIdx.x] = s;
-        sh.hist[(d + 1) & 1][threadIdx.x] = 0;  // the next digit's (read by the cluster before its last sync)
+      meet();
+      // Each CTA adds up its slice of the bins over the cluster (all of them, if it is alone) and tells the others
+      // the slice's sum; the CTA in whose slice the running count reaches `need` tells them the bin.
+      for (int s0 = 0; s0 < kCluster; s0 += ctas) {
+        const int sl = s0 + rank, bin = sl * kSlice + threadIdx.x;
+        int v = 0;
+        if (threadIdx.x < kSlice)
+          for (int r = 0; r < ctas; ++r) v += alone ? hist[bin] : cluster.map_shared_rank(hist, r)[bin];
+        const int incl = warp_incl_scan(v);
+        if (lane == 31 && threadIdx.x < kSlice) sh.warp_sum[warp] = incl;
+        __syncthreads();
+        int sum = 0;
+        for (int i = 0; i < kSlice / 32; ++i) sum += sh.warp_sum[i];
+        if ((int)threadIdx.x < ctas) *(alone ? &sh.slice[sl] : cluster.map_shared_rank(&sh.slice[sl], threadIdx.x)) = sum;
+        __syncthreads();
       }
-      __syncthreads();
-      if (warp == 0) {  // the digit at which the running count reaches `need`
-        int v[8], s = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += (v[i] = sh.total[lane * 8 + i]);
-        const int incl = warp_incl_scan(s);
-        int before = incl - s;
-        if (before < need && need <= incl) {
-          int i = 0;
-          while (before + v[i] < need) before += v[i++];
-          sh.digit = lane * 8 + i;
-          sh.below = before;
+      for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.hist[(d + 1) & 1][i] = 0;  // read before the last meeting
+      meet();
+      int sl = 0, before = 0;
+      while (before + sh.slice[sl] < need) before += sh.slice[sl++];
+      if (sl % ctas == rank) {
+        const int bin = sl * kSlice + threadIdx.x;
+        int v = 0;
+        if (threadIdx.x < kSlice)
+          for (int r = 0; r < ctas; ++r) v += alone ? hist[bin] : cluster.map_shared_rank(hist, r)[bin];
+        const int incl = warp_incl_scan(v);
+        if (lane == 31 && threadIdx.x < kSlice) sh.warp_sum[warp] = incl;
+        __syncthreads();
+        int below_me = before + incl - v;
+        for (int i = 0; i < warp && i < kSlice / 32; ++i) below_me += sh.warp_sum[i];
+        if (below_me < need && need <= below_me + v) {  // one thread
+          for (int r = 0; r < ctas; ++r) {
+            int* f = alone ? sh.found : cluster.map_shared_rank(sh.found, r);
+            f[0] = bin;
+            f[1] = below_me;
+            f[2] = v;
+          }
         }
       }
-      __syncthreads();
-      T |= (uint32_t)sh.digit << shift;
-      need -= sh.below;
-      spare = sh.total[sh.digit] - need;
-      __syncthreads();  // everyone has them before the next digit's are written
+      meet();
+      T |= (uint32_t)sh.found[0] << shift;
+      need -= sh.found[1];
+      spare = sh.found[2] - need;
     }
 
-    // ties before each warp, over the cluster: the first `spare` of them stay
-    int n_tie = 0;
-    for (int t = wlo + lane; t < whi; t += 32) n_tie += t < C && key_at(t) == T;
-    n_tie = warp_sum_i(n_tie);
-    if (lane == 0) sh.ties[warp] = n_tie;
+    if (spare > 0) {  // ties before each warp, over the cluster: the first `spare` of them stay
+      int n_tie = 0;
+      for (int t = wlo + lane; t < whi; t += 32) n_tie += t < C && key_at(t) == T;
+      n_tie = warp_sum_i(n_tie);
+      if (lane == 0) sh.ties[warp] = n_tie;
+      meet();
+    }
   }
-  cluster.sync();
   // sums of the warps before this one in slot order: all of the CTAs before, and of this CTA the warps before
   auto before = [&](int* mine) {
     int s = 0;
-    for (int i = lane; i < kCluster * kSelWarps; i += 32)
-      if (i < rank * kSelWarps + warp) s += cluster.map_shared_rank(mine, i / kSelWarps)[i % kSelWarps];
+    for (int i = lane; i < ctas * kSelWarps; i += 32)
+      if (i < rank * kSelWarps + warp)
+        s += alone ? mine[i] : cluster.map_shared_rank(mine, i / kSelWarps)[i % kSelWarps];
     return warp_sum_i(s);
   };
   const unsigned below = (1u << lane) - 1u;
   int ties0 = 0, n_src = 0, n_hole = 0;
   if (E > 0) {
-    ties0 = before(sh.ties);
+    if (spare > 0) ties0 = before(sh.ties);
     int ties = ties0;
     for (int t0 = wlo; t0 < whi; t0 += 32) {
       const int t = t0 + lane;
@@ -157,9 +188,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
     sh.srcs[warp] = n_src;
     sh.holes[warp] = n_hole;
   }
-  cluster.sync();
+  meet();
   int src0 = before(sh.srcs), hole0 = before(sh.holes);
-  const int last = kCluster * kSelWarps - 1;
+  const int last = ctas * kSelWarps - 1;
   if (rank * kSelWarps + warp == last && lane == 0) ws.counts[b] = src0 + n_src;
   int* src = ws.src + (size_t)b * a.maxp * (kPage / 2);
   int* dst = ws.dst + (size_t)b * a.maxp * (kPage / 2);
@@ -197,68 +228,117 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
     }
   }
   if (me == 0) seq_lens_out[b] = L - E;
-  cluster.sync();  // no CTA leaves while another may read its shared memory
+  if (!alone) cluster.sync();  // no CTA leaves while another may read its shared memory
 }
 
 // ---------------------------------------------------------------------------
-// The moves: grid (x, B), a warp per token row, kRows rows in flight.
+// The moves.  The lists of all sequences are laid end to end in chunks of 32
+// rows and shared evenly by the CTAs; a warp copies four rows of a chunk at a
+// time, every 16-byte piece of them (latent and rope key alike) in flight
+// before the first is stored, and looks up the next four meanwhile.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
 constexpr int kRows = 4;
+constexpr int kChunk = kMoveThreads / 32 * kRows;
+constexpr int kPieces = 3;  // of a row and lane: 96 x 16 bytes a round
 
-template <typename V>
-__device__ __forceinline__ void copy_rows(char* pool, int bytes, const int (&from)[kRows], const int (&to)[kRows]) {
-  const int lane = threadIdx.x & 31;
-  for (int o = lane * (int)sizeof(V); o < bytes; o += 32 * (int)sizeof(V)) {
-    V v[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      if (to[i] >= 0) v[i] = *reinterpret_cast<const V*>(pool + (size_t)from[i] * bytes + o);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      if (to[i] >= 0) *reinterpret_cast<V*>(pool + (size_t)to[i] * bytes + o) = v[i];
-  }
-}
-
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, 2)
     evict_move_kernel(const float* __restrict__ weights, const int* __restrict__ page_table,
                       const int* __restrict__ evict_pages, char* lat, char* rop, float* __restrict__ weights_out,
                       int* __restrict__ err, EvictWorkspace ws, EvictArgs a) {
-  const int b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int count = __ldg(ws.counts + b);
-  if (count == 0) return;
-  const int E = __ldg(evict_pages + b) * kPage;  // count > 0: the select kernel accepted it
   const int slots = a.maxp * kPage;
-  const int* row = page_table + (size_t)b * a.maxp;
-  const int* src = ws.src + (size_t)b * a.maxp * (kPage / 2);
-  const int* dst = ws.dst + (size_t)b * a.maxp * (kPage / 2);
-  const int stride = gridDim.x * (kMoveThreads / 32) * kRows;
-  for (int i0 = (blockIdx.x * (kMoveThreads / 32) + warp) * kRows; i0 < count; i0 += stride) {
-    // lane i < kRows looks up row i0 + i
-    int f = 0, t = -1;
-    if (lane < kRows && i0 + lane < count) {
-      const int s = __ldg(src + i0 + lane), d = __ldg(dst + i0 + lane);
+  // this CTA's chunks, and the sequence of the first
+  auto chunks_of = [&](int b) { return b < a.B ? (__ldg(ws.counts + b) + kChunk - 1) / kChunk : 0; };
+  long long T = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) T += warp_sum_i(chunks_of(b0 + lane));
+  const long long start = worker_start(blockIdx.x, T, gridDim.x);
+  long long left = worker_start(blockIdx.x + 1, T, gridDim.x) - start;
+  if (left == 0) return;
+  int b = 0, c = 0;
+  {
+    long long prefix = 0;
+    for (int b0 = 0;; b0 += 32) {
+      const int k = chunks_of(b0 + lane), incl = warp_incl_scan(k);
+      const unsigned m = __ballot_sync(0xffffffffu, prefix + incl > start);
+      if (m) {
+        const int l = __ffs(m) - 1;
+        b = b0 + l;
+        c = (int)(start - prefix - __shfl_sync(0xffffffffu, incl - k, l));
+        break;
+      }
+      prefix += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  int count = __ldg(ws.counts + b);
+  // lanes 0 .. kRows-1 look up the warp's rows of chunk c of sequence b: the token slots in the pools, to = -1 for
+  // none; the tokens' weights go along
+  int from = 0, to = -1;
+  auto look_up = [&] {
+    from = 0;
+    to = -1;
+    const int i = c * kChunk + warp * kRows + lane;
+    if (lane < kRows && i < count) {
+      const size_t list = (size_t)b * a.maxp * (kPage / 2) + i;
+      const int s = __ldg(ws.src + list), d = __ldg(ws.dst + list);
+      const int* row = page_table + (size_t)b * a.maxp;
       const int pf = __ldg(row + s / kPage), pt = __ldg(row + d / kPage);
-      weights_out[(size_t)b * slots + d - E] = __ldg(weights + (size_t)b * slots + s);
+      // count > 0: evict_pages[b] was accepted
+      weights_out[(size_t)b * slots + d - __ldg(evict_pages + b) * kPage] = __ldg(weights + (size_t)b * slots + s);
       if (pf < 0 || pf >= a.num_pages || pt < 0 || pt >= a.num_pages || __ldg(ws.owners + pt) != 1) {
         report_error(err, kErrDeviceCheck, b, d);  // out of the pool, or another sequence's page too
       } else {
-        f = pf * kPage + s % kPage;
-        t = pt * kPage + d % kPage;
+        from = pf * kPage + s % kPage;
+        to = pt * kPage + d % kPage;
       }
     }
-    int from[kRows], to[kRows];
+  };
+  look_up();
+  const int lat16 = a.lat_bytes / 16;                              // d_c is a multiple of 32
+  const int rop16 = a.rope_bytes % 16 == 0 ? a.rope_bytes / 16 : 0;  // else in words: d_r is even
+  for (; left > 0; --left) {
+    int f[kRows], t[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      from[i] = __shfl_sync(0xffffffffu, f, i);
-      to[i] = __shfl_sync(0xffffffffu, t, i);
+      f[i] = __shfl_sync(0xffffffffu, from, i);
+      t[i] = __shfl_sync(0xffffffffu, to, i);
     }
-    copy_rows<uint4>(lat, a.lat_bytes, from, to);  // d_c is a multiple of 32
-    if (a.rope_bytes % 16 == 0)
-      copy_rows<uint4>(rop, a.rope_bytes, from, to);
-    else
-      copy_rows<uint32_t>(rop, a.rope_bytes, from, to);  // d_r is even
+    if (left > 1) {  // the next chunk's rows
+      if (++c * kChunk >= count) {
+        c = 0;
+        do count = __ldg(ws.counts + ++b);
+        while (count == 0);
+      }
+      look_up();
+    }
+    for (int u0 = 0; u0 < lat16 + rop16; u0 += 32 * kPieces) {
+      uint4 v[kPieces][kRows];
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int u = u0 + 32 * k + lane;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (t[i] >= 0 && u < lat16 + rop16)
+            v[k][i] = *reinterpret_cast<const uint4*>(u < lat16 ? lat + (size_t)f[i] * a.lat_bytes + u * 16
+                                                                : rop + (size_t)f[i] * a.rope_bytes + (u - lat16) * 16);
+      }
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int u = u0 + 32 * k + lane;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (t[i] >= 0 && u < lat16 + rop16)
+            *reinterpret_cast<uint4*>(u < lat16 ? lat + (size_t)t[i] * a.lat_bytes + u * 16
+                                                : rop + (size_t)t[i] * a.rope_bytes + (u - lat16) * 16) = v[k][i];
+      }
+    }
+    if (rop16 == 0)
+      for (int o = lane * 4; o < a.rope_bytes; o += 128)
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (t[i] >= 0)
+            *reinterpret_cast<uint32_t*>(rop + (size_t)t[i] * a.rope_bytes + o) =
+                *reinterpret_cast<const uint32_t*>(rop + (size_t)f[i] * a.rope_bytes + o);
   }
 }
 
@@ -270,7 +350,9 @@ cudaError_t launch_evict(const int* evict_pages, const float* weights, const int
   cudaError_t e = cudaMemsetAsync(ws.owners, 0, (size_t)a.num_pages * sizeof(int), st);
   if (e != cudaSuccess) return e;
   const long long per = ((long long)a.maxp * kPage + kCluster - 1) / kCluster;
-  const int smem = (int)(per < kKeyCap ? per : kKeyCap) * 4;
+  const int slots = a.maxp * kPage;  // a CTA's keys: an eighth of a sequence's, or all of a short one's
+  const long long keys = per < kKeyCap ? (per < kAlone ? (slots < kAlone ? slots : kAlone) : per) : kKeyCap;
+  const int smem = (int)keys * 4;
   e = ensure_smem(reinterpret_cast<const void*>(evict_select_kernel), smem);
   if (e != cudaSuccess) return e;
   evict_select_kernel<<<a.B * kCluster, kSelThreads, smem, st>>>(evict_pages, weights, page_table, seq_lens,
@@ -278,12 +360,11 @@ cudaError_t launch_evict(const int* evict_pages, const float* weights, const int
                                                                  a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // about eight CTAs per SM over all sequences, and no more than the longest list needs
-  const int most = a.maxp * (kPage / 2), rows = kMoveThreads / 32 * kRows;
-  int x = (8 * sms + a.B - 1) / a.B;
-  if (x > (most + rows - 1) / rows) x = (most + rows - 1) / rows;
-  evict_move_kernel<<<dim3(x, a.B), kMoveThreads, 0, st>>>(weights, page_table, evict_pages, static_cast<char*>(lat),
-                                                            static_cast<char*>(rop), weights_out, err, ws, a);
+  // what is resident at once, and no more than there can be chunks
+  const long long most = (long long)a.B * ((a.maxp * (kPage / 2) + kChunk - 1) / kChunk);
+  const int grid = (int)(most < 2 * sms ? most : 2 * sms);
+  evict_move_kernel<<<grid, kMoveThreads, 0, st>>>(weights, page_table, evict_pages, static_cast<char*>(lat),
+                                                   static_cast<char*>(rop), weights_out, err, ws, a);
   return cudaGetLastError();
 }
 
