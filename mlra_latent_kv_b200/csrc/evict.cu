@@ -8,9 +8,9 @@
 // destinations in pages [n, ..): no slot is both, so all moves run at once and
 // in place, and the number of bytes moved is the least that frees those pages.
 //
-// Two kernels.  evict_select_kernel: a cluster of 8 CTAs per sequence finds
+// Two kernels.  evict_select_kernel: a cluster of CTAs per sequence finds
 // the 64 n smallest (weight, slot) by a radix select over the weights' bits
-// (three digits; the CTAs' histograms meet in distributed shared memory)
+// (four 8-bit digits; the CTAs' histograms meet in distributed shared memory)
 // and writes both lists, in slot order, beside the shifted weights, table and
 // length.  It is bound by latency: a sequence's weights are read from HBM once
 // and kept in shared memory.  evict_move_kernel copies the rows, bound by HBM.
@@ -24,10 +24,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kCluster = 8;        // CTAs per sequence
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kKeyCap = 16384;     // keys a CTA keeps in shared memory (a sequence of 131072 tokens); longer: re-read
+constexpr int kKeyCap = 24576;     // keys a CTA keeps in shared memory, two CTAs per SM; beyond: re-read
 
 // Ascending order of the weights as unsigned integers: -inf and NaN first, -0 equal to +0.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -36,22 +35,19 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kBins = 2048;        // of a digit: 11, 11 and 10 bits
-constexpr int kSlice = kBins / kCluster;  // bins that a CTA adds up for the cluster
+constexpr int kBins = 256;         // of a digit
+constexpr int kBatch = 8;          // keys a thread handles at once
 constexpr int kAlone = 4096;       // a sequence that one CTA takes alone, without the cluster's barriers
-static_assert(kSlice % 32 == 0 && kSlice <= kSelThreads, "a thread per bin of a slice");
-
 struct SelShared {
   int hist[2][kBins];          // of this CTA, double-buffered over the digits
-  int warp_sum[kSelWarps];
+  int warp_sum[kBins / 32];
   int ties[kSelWarps];         // equal to the threshold, per warp
   int srcs[kSelWarps];         // tokens to move, per warp
   int holes[kSelWarps];        // slots to move to, per warp
-  int slice[kCluster];         // keys in each CTA's slice of the bins
   int found[3];                // the digit, the keys below it, the keys that have it
 };
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, 2)
     evict_select_kernel(const int* __restrict__ evict_pages, const float* __restrict__ weights,
                         const int* __restrict__ page_table, const int* __restrict__ seq_lens,
                         float* __restrict__ weights_out, int* __restrict__ page_table_out,
@@ -59,7 +55,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) SelShared sh;
   cg::cluster_group cluster = cg::this_cluster();
-  const int b = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+  const int cl = cluster.num_blocks();  // CTAs per sequence
+  const int b = blockIdx.x / cl, rank = cluster.block_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slots = a.maxp * kPage;
   const float* w = weights + (size_t)b * slots;
@@ -74,8 +71,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
   const int C = n > 0 ? L - a.recent : 0;  // tokens that may leave: slots [0, C)
 
   // this CTA's slots, and within them each warp's
-  const bool alone = L <= kAlone;
-  const int ctas = alone ? 1 : kCluster;
+  const bool alone = L <= kAlone || cl == 1;
+  const int ctas = alone ? 1 : cl;
   auto meet = [&] {  // all CTAs that share the sequence
     if (alone)
       __syncthreads();
@@ -87,72 +84,76 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
   const bool in_smem = per <= kKeyCap;
   const int wper = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int wlo = min(hi, lo + warp * wper), whi = min(hi, wlo + wper);
-  auto key_at = [&](int t) { return in_smem ? keys[t - lo] : order_key(__ldg(w + t)); };
+  // the keys of slots t, t + stride, .. of this CTA, read at once (0 past its last)
+  auto keys_at = [&](int t, int stride, uint32_t (&u)[kBatch]) {
+    if (in_smem) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) u[i] = t + i * stride < hi ? keys[t + i * stride - lo] : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) u[i] = t + i * stride < hi ? order_key(__ldg(w + t + i * stride)) : 0u;
+    }
+  };
 
   uint32_t T = 0;  // the largest key that leaves
   int spare = 0;   // of the tokens with that key, in slot order, the first `spare` stay
   if (E > 0 && rank < ctas) {  // uniform over the CTAs that meet
     if (in_smem)
-      for (int t = lo + threadIdx.x; t < hi; t += kSelThreads) keys[t - lo] = order_key(__ldg(w + t));
+      for (int t0 = lo + threadIdx.x; t0 < hi; t0 += 2 * kBatch * kSelThreads) {
+        float x[2 * kBatch];
+#pragma unroll
+        for (int i = 0; i < 2 * kBatch; ++i)
+          if (t0 + i * kSelThreads < hi) x[i] = __ldg(w + t0 + i * kSelThreads);
+#pragma unroll
+        for (int i = 0; i < 2 * kBatch; ++i)
+          if (t0 + i * kSelThreads < hi) keys[t0 + i * kSelThreads - lo] = order_key(x[i]);
+      }
     for (int i = threadIdx.x; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
     __syncthreads();
     int need = E;  // how many of the keys that share the digits found so far leave
-    for (int d = 0; d < 3; ++d) {
-      const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
-      const uint32_t digits = d == 2 ? 1023u : 2047u, mask = d == 0 ? 0u : 0xFFFFFFFFu << (d == 1 ? 21 : 10);
+    for (int d = 0; d < 4; ++d) {
+      const int shift = 24 - 8 * d;
+      const uint32_t mask = d == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
       int* hist = sh.hist[d & 1];
-      for (int t = lo + threadIdx.x; t < min(hi, C); t += kSelThreads) {
-        const uint32_t u = key_at(t);
-        if ((u & mask) == T) atomicAdd(&hist[(u >> shift) & digits], 1);
+      const int end = min(hi, C);
+      for (int t0 = lo + threadIdx.x; t0 < end; t0 += kBatch * kSelThreads) {
+        uint32_t u[kBatch];
+        keys_at(t0, kSelThreads, u);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (t0 + i * kSelThreads < end && (u[i] & mask) == T) atomicAdd(&hist[(u[i] >> shift) & 255u], 1);
       }
       meet();
-      // Each CTA adds up its slice of the bins over the cluster (all of them, if it is alone) and tells the others
-      // the slice's sum; the CTA in whose slice the running count reaches `need` tells them the bin.
-      for (int s0 = 0; s0 < kCluster; s0 += ctas) {
-        const int sl = s0 + rank, bin = sl * kSlice + threadIdx.x;
-        int v = 0;
-        if (threadIdx.x < kSlice)
-          for (int r = 0; r < ctas; ++r) v += alone ? hist[bin] : cluster.map_shared_rank(hist, r)[bin];
-        const int incl = warp_incl_scan(v);
-        if (lane == 31 && threadIdx.x < kSlice) sh.warp_sum[warp] = incl;
-        __syncthreads();
-        int sum = 0;
-        for (int i = 0; i < kSlice / 32; ++i) sum += sh.warp_sum[i];
-        if ((int)threadIdx.x < ctas) *(alone ? &sh.slice[sl] : cluster.map_shared_rank(&sh.slice[sl], threadIdx.x)) = sum;
-        __syncthreads();
+      int v = 0;
+      if (threadIdx.x < kBins) {  // a thread per bin: its count over the cluster, and the running count
+        for (int r = 0; r < ctas; ++r) v += alone ? hist[threadIdx.x] : cluster.map_shared_rank(hist, r)[threadIdx.x];
+        sh.hist[(d + 1) & 1][threadIdx.x] = 0;  // the next digit's: read before this meeting
       }
-      for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.hist[(d + 1) & 1][i] = 0;  // read before the last meeting
-      meet();
-      int sl = 0, before = 0;
-      while (before + sh.slice[sl] < need) before += sh.slice[sl++];
-      if (sl % ctas == rank) {
-        const int bin = sl * kSlice + threadIdx.x;
-        int v = 0;
-        if (threadIdx.x < kSlice)
-          for (int r = 0; r < ctas; ++r) v += alone ? hist[bin] : cluster.map_shared_rank(hist, r)[bin];
-        const int incl = warp_incl_scan(v);
-        if (lane == 31 && threadIdx.x < kSlice) sh.warp_sum[warp] = incl;
-        __syncthreads();
-        int below_me = before + incl - v;
-        for (int i = 0; i < warp && i < kSlice / 32; ++i) below_me += sh.warp_sum[i];
-        if (below_me < need && need <= below_me + v) {  // one thread
-          for (int r = 0; r < ctas; ++r) {
-            int* f = alone ? sh.found : cluster.map_shared_rank(sh.found, r);
-            f[0] = bin;
-            f[1] = below_me;
-            f[2] = v;
-          }
-        }
+      const int incl = warp_incl_scan(v);
+      if (lane == 31 && threadIdx.x < kBins) sh.warp_sum[warp] = incl;
+      __syncthreads();
+      int below_me = incl - v;
+      for (int i = 0; i < warp && i < kBins / 32; ++i) below_me += sh.warp_sum[i];
+      if (below_me < need && need <= below_me + v) {  // one thread: the count reaches `need` here
+        sh.found[0] = threadIdx.x;
+        sh.found[1] = below_me;
+        sh.found[2] = v;
       }
-      meet();
+      __syncthreads();
       T |= (uint32_t)sh.found[0] << shift;
       need -= sh.found[1];
       spare = sh.found[2] - need;
+      __syncthreads();  // everyone has them before the next digit's are written
     }
 
     if (spare > 0) {  // ties before each warp, over the cluster: the first `spare` of them stay
       int n_tie = 0;
-      for (int t = wlo + lane; t < whi; t += 32) n_tie += t < C && key_at(t) == T;
+      for (int t0 = wlo + lane; t0 < whi; t0 += 32 * kBatch) {
+        uint32_t u[kBatch];
+        keys_at(t0, 32, u);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) n_tie += t0 + 32 * i < min(whi, C) && u[i] == T;
+      }
       n_tie = warp_sum_i(n_tie);
       if (lane == 0) sh.ties[warp] = n_tie;
       meet();
@@ -168,19 +169,28 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
   };
   const unsigned below = (1u << lane) - 1u;
   int ties0 = 0, n_src = 0, n_hole = 0;
+  // this warp's slots in order, 32 at a time, each with whether its token leaves (false past the warp's last)
+  auto walk = [&](auto f) {
+    int ties = ties0;
+    for (int t0 = wlo + lane; t0 - lane < whi; t0 += 32 * kBatch) {
+      uint32_t u[kBatch];
+      keys_at(t0, 32, u);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int t = t0 + 32 * i;
+        const bool may = t < min(whi, C), tie = may && u[i] == T;
+        const unsigned tm = __ballot_sync(0xffffffffu, tie);
+        f(t, may && (u[i] < T || (tie && ties + __popc(tm & below) >= spare)));
+        ties += __popc(tm);
+      }
+    }
+  };
   if (E > 0) {
     if (spare > 0) ties0 = before(sh.ties);
-    int ties = ties0;
-    for (int t0 = wlo; t0 < whi; t0 += 32) {
-      const int t = t0 + lane;
-      const uint32_t u = t < whi ? key_at(t) : 0u;
-      const bool tie = t < whi && t < C && u == T;
-      const unsigned tm = __ballot_sync(0xffffffffu, tie);
-      const bool gone = t < whi && t < C && (u < T || (tie && ties + __popc(tm & below) >= spare));
-      ties += __popc(tm);
-      n_src += t < whi && t < E && !gone;
+    walk([&](int t, bool gone) {
+      n_src += t < min(whi, E) && !gone;
       n_hole += t >= E && gone;
-    }
+    });
     n_src = warp_sum_i(n_src);
     n_hole = warp_sum_i(n_hole);
   }
@@ -194,31 +204,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
   if (rank * kSelWarps + warp == last && lane == 0) ws.counts[b] = src0 + n_src;
   int* src = ws.src + (size_t)b * a.maxp * (kPage / 2);
   int* dst = ws.dst + (size_t)b * a.maxp * (kPage / 2);
-  float* wo = weights_out + (size_t)b * slots;
-  {
-    int ties = ties0;
-    for (int t0 = wlo; t0 < whi; t0 += 32) {
-      const int t = t0 + lane;
-      bool gone = false;
-      if (E > 0) {
-        const uint32_t u = t < whi ? key_at(t) : 0u;
-        const bool tie = t < whi && t < C && u == T;
-        const unsigned tm = __ballot_sync(0xffffffffu, tie);
-        gone = t < whi && t < C && (u < T || (tie && ties + __popc(tm & below) >= spare));
-        ties += __popc(tm);
-      }
-      const bool moves = t < whi && t < E && !gone, hole = t >= E && gone;
+  if (E > 0)
+    walk([&](int t, bool gone) {
+      const bool moves = t < min(whi, E) && !gone, hole = t >= E && gone;
       const unsigned sm = __ballot_sync(0xffffffffu, moves), hm = __ballot_sync(0xffffffffu, hole);
       if (moves) src[src0 + __popc(sm & below)] = t;
       if (hole) dst[hole0 + __popc(hm & below)] = t;
       src0 += __popc(sm);
       hole0 += __popc(hm);
-      if (t < whi && t >= E && !hole) wo[t - E] = __ldg(w + t);  // a hole's weight comes with the token
-    }
-  }
-  // behind the sequence: zeros; the table without its first n entries
-  const int all = kCluster * kSelThreads, me = rank * kSelThreads + threadIdx.x;
-  for (int t = L - E + me; t < slots; t += all) wo[t] = 0.f;
+    });
+  // the weights in their new places, zeros behind them (a moved token's weight comes with it, over the one that
+  // was there); the table without its first n entries
+  const int all = cl * kSelThreads, me = rank * kSelThreads + threadIdx.x;
+  float* wo = weights_out + (size_t)b * slots;
+#pragma unroll 4
+  for (int t = me; t < slots; t += all) wo[t] = t + E < L ? __ldg(w + t + E) : 0.f;
   const int* row = page_table + (size_t)b * a.maxp;
   for (int p = me; p < a.maxp; p += all) {
     page_table_out[(size_t)b * a.maxp + p] = p + n < a.maxp ? __ldg(row + p + n) : -1;
@@ -349,16 +349,30 @@ cudaError_t launch_evict(const int* evict_pages, const float* weights, const int
                          const EvictWorkspace& ws, const EvictArgs& a, int sms, cudaStream_t st) {
   cudaError_t e = cudaMemsetAsync(ws.owners, 0, (size_t)a.num_pages * sizeof(int), st);
   if (e != cudaSuccess) return e;
-  const long long per = ((long long)a.maxp * kPage + kCluster - 1) / kCluster;
-  const int slots = a.maxp * kPage;  // a CTA's keys: an eighth of a sequence's, or all of a short one's
-  const long long keys = per < kKeyCap ? (per < kAlone ? (slots < kAlone ? slots : kAlone) : per) : kKeyCap;
-  const int smem = (int)keys * 4;
-  e = ensure_smem(reinterpret_cast<const void*>(evict_select_kernel), smem);
+  // A cluster as large as two resident CTAs per SM allow: a few long sequences spread over 16 CTAs each (four of
+  // 131072 tokens: 35 us with 8), many over fewer, so that they run in one wave (64 sequences: 35 us with 8).
+  int cl = 16;
+  while (cl > 1 && (long long)a.B * cl > 2LL * sms) cl /= 2;
+  const int slots = a.maxp * kPage, per = (slots + cl - 1) / cl;  // a CTA's keys: its part of a sequence's,
+  const int alone = slots < kAlone ? slots : kAlone;              // or all of a short one's
+  const int keys = per < kKeyCap ? (per < alone ? alone : per) : kKeyCap;
+  e = ensure_smem(reinterpret_cast<const void*>(evict_select_kernel), keys * 4);
+  if (e == cudaSuccess && cl > 8)
+    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  evict_select_kernel<<<a.B * kCluster, kSelThreads, smem, st>>>(evict_pages, weights, page_table, seq_lens,
-                                                                 weights_out, page_table_out, seq_lens_out, err, ws,
-                                                                 a);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.B * cl);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = keys * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cl;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, evict_pages, weights, page_table, seq_lens, weights_out,
+                         page_table_out, seq_lens_out, err, ws, a);
   if (e != cudaSuccess) return e;
   // what is resident at once, and no more than there can be chunks
   const long long most = (long long)a.B * ((a.maxp * (kPage / 2) + kChunk - 1) / kChunk);
