@@ -63,7 +63,9 @@ extern "C" {
  *   out [total_q, H, d_v] dense   lse [total_q, H] fp32 dense, or NULL
  * dims: n_branch must be 1; d_c is not used; d_v <= 512.  A sequence whose
  * offsets are out of range, or whose Lk the page table cannot hold, is
- * reported (mlra_check_status) and gets no output.
+ * reported (mlra_check_status) and gets no output; so is a batch whose
+ * sequences overlap so far that they have more than total_q rows together, and
+ * then its outputs are void.
  * Kernel AUTO runs the tcgen05 kernel for bf16, d_h = 128, d_r = 64,
  * d_v = 128 with every stride a multiple of 8 elements, and the CUDA-core
  * kernel otherwise.

@@ -49,6 +49,11 @@ __global__ void __launch_bounds__(kPThreads)
       if (t < n) break;
       t -= n;
     }
+    // the grid has a tile more than sequences that do not overlap can have
+    if (blockIdx.x == gridDim.x - 1 && b < a.B) {
+      report_error(err, kErrDeviceCheck, a.B, a.total_q);
+      b = a.B;
+    }
     s_b = b;
     s_tile = t;
   }

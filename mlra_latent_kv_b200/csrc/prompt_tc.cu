@@ -107,14 +107,28 @@ __global__ void __launch_bounds__(kPlanThreads)
   grid_dep_launch();
   if (blockIdx.x == 0) {
     __shared__ int bins[kPlanBins], s_most, s_warp[32];
+    __shared__ unsigned long long s_rows;
     for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) bins[i] = 0;
-    if (threadIdx.x == 0) s_most = 1;
+    if (threadIdx.x == 0) {
+      s_most = 1;
+      s_rows = 0;
+    }
     __syncthreads();
     for (int b = threadIdx.x; b < a.B; b += kPlanThreads) {
       const PromptSeq s = prompt_seq(cu_q, cu_k, b, a, err);
-      if (s.Lq > 0) atomicMax(&s_most, (s.Lk + 127) / 128);
+      if (s.Lq > 0) {
+        atomicMax(&s_most, (s.Lk + 127) / 128);
+        atomicAdd(&s_rows, (unsigned long long)s.Lq);
+      }
     }
     __syncthreads();
+    if (s_rows > (unsigned long long)a.total_q) {  // sequences that overlap: the list has no room for them
+      if (threadIdx.x == 0) {
+        report_error(err, kErrDeviceCheck, a.B, a.total_q);
+        counts[0] = counts[1] = 0;
+      }
+      return;
+    }
     const int most = s_most;
     // bin 0 holds the longest; an order within a bin is as good as another
     auto bin = [&](const PromptSeq& s, int pair) {
@@ -157,8 +171,17 @@ __global__ void __launch_bounds__(kPlanThreads)
       else
         hi = mid - 1;
     }
-    const PromptSeq s = prompt_seq(cu_q, cu_k, lo, a, nullptr);
-    if (t < s.q0 || t >= s.q0 + s.Lq) continue;
+    PromptSeq s = prompt_seq(cu_q, cu_k, lo, a, nullptr);
+    auto holds = [&] { return t >= s.q0 && t < s.q0 + s.Lq; };
+    if (!holds()) {  // a row of no sequence, or bad offsets led the search astray: all of them, a lane each
+      unsigned found = 0;
+      for (int b0 = 0; b0 < a.B && !found; b0 += 32) {
+        if (b0 + lane < a.B) s = prompt_seq(cu_q, cu_k, b0 + lane, a, nullptr);
+        found = __ballot_sync(0xffffffffu, b0 + lane < a.B && holds());
+        if (found) s = prompt_seq(cu_q, cu_k, b0 + __ffs(found) - 1, a, nullptr);
+      }
+      if (!found) continue;
+    }
     float sn, cs;
     rope_sincos(tab, lane, s.Lk - s.Lq + t - s.q0, &sn, &cs);
     const int c = lane & 7;  // this lane's 16 bytes of a head: pairs 4 c .. 4 c + 3

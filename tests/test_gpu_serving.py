@@ -230,6 +230,31 @@ def test_prompt_offsets_out_of_range_are_reported(dtype):
     abi.check_status(p.ws)  # and cleared
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_bad_offset_between_good_ones(dtype):
+    p = Prompt(dtype, (50, 60, 70, 40), (50, 60, 70, 40), 2, 2, dims=FULL if dtype == "bf16" else TINY, seed=7)
+    p.call()
+    want = p.out.clone()
+    p.out.fill_(float("nan"))
+    p.ws.zero_()
+    p.cu_q[2] = 10000  # the second and the third sequence have no rows
+    p.call()
+    with pytest.raises(abi.MlraError):
+        abi.check_status(p.ws)
+    for rows in (slice(0, 50), slice(180, 220)):
+        assert torch.equal(p.out[rows], want[rows])
+    assert torch.isnan(p.out[50:180].float()).all() and torch.isnan(p.out[220:].float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_overlapping_sequences_are_reported(dtype):
+    p = Prompt(dtype, (50, 60, 70), (50, 60, 70), 2, 2, dims=FULL if dtype == "bf16" else TINY, seed=7)
+    p.cu_q[:] = torch.tensor([0, 180, 0, 180], dtype=torch.int32)  # the third goes over the first one's rows again
+    p.call()
+    with pytest.raises(abi.MlraError):
+        abi.check_status(p.ws)
+
+
 def test_prompt_bad_page_is_reported():
     for dtype, dims in (("f32", TINY), ("bf16", FULL)):
         p = Prompt(dtype, (50, 100), (50, 100), 2, 2, dims=dims, seed=8)
