@@ -778,10 +778,14 @@ cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* 
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
-  // units of heads whose K and V (256 values a token and kv head) take about 48 MB of L2 together
+  // Units of heads whose K and V (256 values a token and kv head) fit in 112 of L2's 126 MB together, in groups of
+  // one size: a last group of few heads is a long wait for its longest items (64 heads x 4096 tokens: 345 us as
+  // 48 + 16, 321 as 32 + 32; 32 heads: 188 us as 24 + 8, 165 as one; 128 heads: 694 us as one, 647 as 43 + 43 + 42).
   const long long bytes = (long long)a.total_k * 512 * a.kv_heads / units;
-  long long group = bytes > 0 ? (48LL << 20) / bytes : units;
+  long long group = bytes > 0 ? (112LL << 20) / bytes : units;
   group = group < 1 ? 1 : (group > units ? units : group);
+  const long long groups = (units + group - 1) / group;
+  group = (units + groups - 1) / groups;
   // what the roles are dealt has to be there: the kernel's registers at launch
   static const int regs = [] {
     cudaFuncAttributes f;
