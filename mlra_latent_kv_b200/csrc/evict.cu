@@ -8,7 +8,8 @@
 // destinations in pages [n, ..): no slot is both, so all moves run at once and
 // in place, and the number of bytes moved is the least that frees those pages.
 //
-// Two kernels.  evict_select_kernel: a cluster of CTAs per sequence finds
+// Two kernels, after one that clears the pages' owner counts.
+// evict_select_kernel: a cluster of CTAs per sequence finds
 // the 64 n smallest (weight, slot) by a radix select over the weights' bits
 // (four 8-bit digits; the CTAs' histograms meet in distributed shared memory)
 // and writes both lists, in slot order, beside the shifted weights, table and
@@ -17,6 +18,7 @@
 #include <cooperative_groups.h>
 
 #include "host_cache.h"
+#include "ptx.cuh"
 #include "serving.h"
 
 namespace mlra {
@@ -52,6 +54,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
                         const int* __restrict__ page_table, const int* __restrict__ seq_lens,
                         float* __restrict__ weights_out, int* __restrict__ page_table_out,
                         int* __restrict__ seq_lens_out, int* __restrict__ err, EvictWorkspace ws, EvictArgs a) {
+  ptx::grid_dep_launch();
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) SelShared sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -220,6 +223,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
 #pragma unroll 4
   for (int t = me; t < slots; t += all) wo[t] = t + E < L ? __ldg(w + t + E) : 0.f;
   const int* row = page_table + (size_t)b * a.maxp;
+  ptx::grid_dep_wait();  // the owners are cleared
   for (int p = me; p < a.maxp; p += all) {
     page_table_out[(size_t)b * a.maxp + p] = p + n < a.maxp ? __ldg(row + p + n) : -1;
     if (p * kPage < L) {
@@ -232,114 +236,115 @@ __global__ void __launch_bounds__(kSelThreads, 2)
 }
 
 // ---------------------------------------------------------------------------
-// The moves.  The lists of all sequences are laid end to end in chunks of 32
-// rows and shared evenly by the CTAs; a warp copies four rows of a chunk at a
-// time, every 16-byte piece of them (latent and rope key alike) in flight
-// before the first is stored, and looks up the next four meanwhile.
+// The moves.  The lists of all sequences are laid end to end and shared evenly
+// by the warps, to the row.  A warp looks up 32 rows at once (a chain of three
+// loads: list, page table, owners) and copies them four at a time, every
+// 16-byte piece of the four (latent and rope key alike) in flight before the
+// first is stored.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
 constexpr int kRows = 4;
-constexpr int kChunk = kMoveThreads / 32 * kRows;
 constexpr int kPieces = 3;  // of a row and lane: 96 x 16 bytes a round
 
 __global__ void __launch_bounds__(kMoveThreads, 2)
     evict_move_kernel(const float* __restrict__ weights, const int* __restrict__ page_table,
                       const int* __restrict__ evict_pages, char* lat, char* rop, float* __restrict__ weights_out,
                       int* __restrict__ err, EvictWorkspace ws, EvictArgs a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const int slots = a.maxp * kPage;
-  // this CTA's chunks, and the sequence of the first
-  auto chunks_of = [&](int b) { return b < a.B ? (__ldg(ws.counts + b) + kChunk - 1) / kChunk : 0; };
+  ptx::grid_dep_wait();  // the lists
+  // this warp's rows, and the sequence of the first
+  auto rows_of = [&](int b) { return b < a.B ? __ldcg(ws.counts + b) : 0; };
   long long T = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) T += warp_sum_i(chunks_of(b0 + lane));
-  const long long start = worker_start(blockIdx.x, T, gridDim.x);
-  long long left = worker_start(blockIdx.x + 1, T, gridDim.x) - start;
+  for (int b0 = 0; b0 < a.B; b0 += 32) T += warp_sum_i(rows_of(b0 + lane));
+  const int w = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5), W = gridDim.x * (kMoveThreads / 32);
+  const long long start = worker_start(w, T, W);
+  int left = (int)(worker_start(w + 1, T, W) - start);
   if (left == 0) return;
-  int b = 0, c = 0;
+  int b = 0, i = 0, count = 0;
   {
     long long prefix = 0;
     for (int b0 = 0;; b0 += 32) {
-      const int k = chunks_of(b0 + lane), incl = warp_incl_scan(k);
+      const int k = rows_of(b0 + lane), incl = warp_incl_scan(k);
       const unsigned m = __ballot_sync(0xffffffffu, prefix + incl > start);
       if (m) {
         const int l = __ffs(m) - 1;
         b = b0 + l;
-        c = (int)(start - prefix - __shfl_sync(0xffffffffu, incl - k, l));
+        count = __shfl_sync(0xffffffffu, k, l);
+        i = (int)(start - prefix) - __shfl_sync(0xffffffffu, incl - k, l);
         break;
       }
       prefix += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  int count = __ldg(ws.counts + b);
-  // lanes 0 .. kRows-1 look up the warp's rows of chunk c of sequence b: the token slots in the pools, to = -1 for
-  // none; the tokens' weights go along
-  int from = 0, to = -1;
-  auto look_up = [&] {
-    from = 0;
-    to = -1;
-    const int i = c * kChunk + warp * kRows + lane;
-    if (lane < kRows && i < count) {
-      const size_t list = (size_t)b * a.maxp * (kPage / 2) + i;
-      const int s = __ldg(ws.src + list), d = __ldg(ws.dst + list);
+  const int lat16 = a.lat_bytes / 16;                              // d_c is a multiple of 32
+  const int rop16 = a.rope_bytes % 16 == 0 ? a.rope_bytes / 16 : 0;  // else in words: d_r is even
+  while (left > 0) {
+    while (i == count) {
+      count = __ldcg(ws.counts + ++b);
+      i = 0;
+    }
+    const int n = min(32, min(count - i, left));  // rows of this round, a lane each
+    int from = 0, to = -1;  // their token slots in the pools, to = -1 for none; the tokens' weights go along
+    if (lane < n) {
+      const size_t list = (size_t)b * a.maxp * (kPage / 2) + i + lane;
+      const int s = __ldcg(ws.src + list), d = __ldcg(ws.dst + list);
       const int* row = page_table + (size_t)b * a.maxp;
       const int pf = __ldg(row + s / kPage), pt = __ldg(row + d / kPage);
       // count > 0: evict_pages[b] was accepted
       weights_out[(size_t)b * slots + d - __ldg(evict_pages + b) * kPage] = __ldg(weights + (size_t)b * slots + s);
-      if (pf < 0 || pf >= a.num_pages || pt < 0 || pt >= a.num_pages || __ldg(ws.owners + pt) != 1) {
+      if (pf < 0 || pf >= a.num_pages || pt < 0 || pt >= a.num_pages || __ldcg(ws.owners + pt) != 1) {
         report_error(err, kErrDeviceCheck, b, d);  // out of the pool, or another sequence's page too
       } else {
         from = pf * kPage + s % kPage;
         to = pt * kPage + d % kPage;
       }
     }
-  };
-  look_up();
-  const int lat16 = a.lat_bytes / 16;                              // d_c is a multiple of 32
-  const int rop16 = a.rope_bytes % 16 == 0 ? a.rope_bytes / 16 : 0;  // else in words: d_r is even
-  for (; left > 0; --left) {
-    int f[kRows], t[kRows];
+    i += n;
+    left -= n;
+    for (int r = 0; r < n; r += kRows) {
+      int f[kRows], t[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      f[i] = __shfl_sync(0xffffffffu, from, i);
-      t[i] = __shfl_sync(0xffffffffu, to, i);
-    }
-    if (left > 1) {  // the next chunk's rows
-      if (++c * kChunk >= count) {
-        c = 0;
-        do count = __ldg(ws.counts + ++b);
-        while (count == 0);
+      for (int k = 0; k < kRows; ++k) {
+        f[k] = __shfl_sync(0xffffffffu, from, r + k);  // past the last row: to = -1
+        t[k] = __shfl_sync(0xffffffffu, to, r + k);
       }
-      look_up();
-    }
-    for (int u0 = 0; u0 < lat16 + rop16; u0 += 32 * kPieces) {
-      uint4 v[kPieces][kRows];
+      for (int u0 = 0; u0 < lat16 + rop16; u0 += 32 * kPieces) {
+        uint4 v[kPieces][kRows];
 #pragma unroll
-      for (int k = 0; k < kPieces; ++k) {
-        const int u = u0 + 32 * k + lane;
+        for (int k = 0; k < kPieces; ++k) {
+          const int u = u0 + 32 * k + lane;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-          if (t[i] >= 0 && u < lat16 + rop16)
-            v[k][i] = *reinterpret_cast<const uint4*>(u < lat16 ? lat + (size_t)f[i] * a.lat_bytes + u * 16
-                                                                : rop + (size_t)f[i] * a.rope_bytes + (u - lat16) * 16);
+          for (int q = 0; q < kRows; ++q)
+            if (t[q] >= 0 && u < lat16 + rop16)
+              v[k][q] = *reinterpret_cast<const uint4*>(
+                  u < lat16 ? lat + (size_t)f[q] * a.lat_bytes + u * 16
+                            : rop + (size_t)f[q] * a.rope_bytes + (u - lat16) * 16);
+        }
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+          const int u = u0 + 32 * k + lane;
+#pragma unroll
+          for (int q = 0; q < kRows; ++q)
+            if (t[q] >= 0 && u < lat16 + rop16)
+              *reinterpret_cast<uint4*>(u < lat16 ? lat + (size_t)t[q] * a.lat_bytes + u * 16
+                                                  : rop + (size_t)t[q] * a.rope_bytes + (u - lat16) * 16) = v[k][q];
+        }
       }
+      if (rop16 == 0)
+        for (int o = lane * 4; o < a.rope_bytes; o += 128)
 #pragma unroll
-      for (int k = 0; k < kPieces; ++k) {
-        const int u = u0 + 32 * k + lane;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-          if (t[i] >= 0 && u < lat16 + rop16)
-            *reinterpret_cast<uint4*>(u < lat16 ? lat + (size_t)t[i] * a.lat_bytes + u * 16
-                                                : rop + (size_t)t[i] * a.rope_bytes + (u - lat16) * 16) = v[k][i];
-      }
+          for (int q = 0; q < kRows; ++q)
+            if (t[q] >= 0)
+              *reinterpret_cast<uint32_t*>(rop + (size_t)t[q] * a.rope_bytes + o) =
+                  *reinterpret_cast<const uint32_t*>(rop + (size_t)f[q] * a.rope_bytes + o);
     }
-    if (rop16 == 0)
-      for (int o = lane * 4; o < a.rope_bytes; o += 128)
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-          if (t[i] >= 0)
-            *reinterpret_cast<uint32_t*>(rop + (size_t)t[i] * a.rope_bytes + o) =
-                *reinterpret_cast<const uint32_t*>(rop + (size_t)f[i] * a.rope_bytes + o);
   }
+}
+
+__global__ void __launch_bounds__(1024) evict_clear_kernel(int* owners, int n) {
+  ptx::grid_dep_launch();
+  for (int i = blockIdx.x * 1024 + threadIdx.x; i < n; i += gridDim.x * 1024) owners[i] = 0;
 }
 
 }  // namespace
@@ -347,13 +352,19 @@ __global__ void __launch_bounds__(kMoveThreads, 2)
 cudaError_t launch_evict(const int* evict_pages, const float* weights, const int* page_table, const int* seq_lens,
                          void* lat, void* rop, float* weights_out, int* page_table_out, int* seq_lens_out, int* err,
                          const EvictWorkspace& ws, const EvictArgs& a, int sms, cudaStream_t st) {
-  cudaError_t e = cudaMemsetAsync(ws.owners, 0, (size_t)a.num_pages * sizeof(int), st);
+  // Each kernel is launched while the one before still runs and waits for what it needs of it.
+  const int clear = (a.num_pages + 1023) / 1024;
+  evict_clear_kernel<<<clear < sms ? clear : sms, 1024, 0, st>>>(ws.owners, a.num_pages);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // A cluster as large as two resident CTAs per SM allow: a few long sequences spread over 16 CTAs each (four of
-  // 131072 tokens: 35 us with 8), many over fewer, so that they run in one wave (64 sequences: 35 us with 8).
+  // 131072 tokens: 35 us with 8), many over fewer, so that they run in one wave (64 sequences: 35 us with 8).  No
+  // cluster where no sequence can be longer than what one CTA takes alone.
   int cl = 16;
   while (cl > 1 && (long long)a.B * cl > 2LL * sms) cl /= 2;
-  const int slots = a.maxp * kPage, per = (slots + cl - 1) / cl;  // a CTA's keys: its part of a sequence's,
+  const int slots = a.maxp * kPage;
+  if (slots <= kAlone) cl = 1;
+  const int per = (slots + cl - 1) / cl;  // a CTA's keys: its part of a sequence's,
   const int alone = slots < kAlone ? slots : kAlone;              // or all of a short one's
   const int keys = per < kKeyCap ? (per < alone ? alone : per) : kKeyCap;
   e = ensure_smem(reinterpret_cast<const void*>(evict_select_kernel), keys * 4);
@@ -365,21 +376,25 @@ cudaError_t launch_evict(const int* evict_pages, const float* weights, const int
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = keys * 4;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cl;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cl;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, evict_pages, weights, page_table, seq_lens, weights_out,
                          page_table_out, seq_lens_out, err, ws, a);
   if (e != cudaSuccess) return e;
-  // what is resident at once, and no more than there can be chunks
-  const long long most = (long long)a.B * ((a.maxp * (kPage / 2) + kChunk - 1) / kChunk);
-  const int grid = (int)(most < 2 * sms ? most : 2 * sms);
-  evict_move_kernel<<<grid, kMoveThreads, 0, st>>>(weights, page_table, evict_pages, static_cast<char*>(lat),
-                                                   static_cast<char*>(rop), weights_out, err, ws, a);
-  return cudaGetLastError();
+  // what is resident at once, and no more than there can be rows
+  const long long most = ((long long)a.B * a.maxp * (kPage / 2) + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
+  cfg.gridDim = dim3((unsigned)(most < 2 * sms ? most : 2 * sms));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, weights, page_table, evict_pages, static_cast<char*>(lat),
+                            static_cast<char*>(rop), weights_out, err, ws, a);
 }
 
 }  // namespace mlra
