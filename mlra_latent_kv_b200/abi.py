@@ -283,7 +283,7 @@ def _refuse(name, x, shape, dtype, strided, device):
     import torch
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         why = "has to be a CUDA tensor"
-    elif device is not None and x.get_device() != device:
+    elif x.get_device() != device:
         why = f"is on {x.device}, others on cuda:{device}"
     elif x.dtype is not dtype:
         why = f"is {x.dtype}, not {dtype}"
@@ -299,25 +299,27 @@ def _run(fn, dims, stream, workspace, tensors, lead=(), strided=()):
     layout and a common device before anything is enqueued) and the workspace, on the tensors' device.  An entry
     whose tensor is None passes NULL."""
     import torch
-    device, args = None, []
+    first = tensors[0][1]
+    device = first.get_device() if isinstance(first, torch.Tensor) else -1
+    args = []
     for name, x, shape, dtype in tensors:
         if x is None:
             args.append(None)
             continue
         try:
-            ok = x.dtype is dtype and x.shape == shape and x.is_cuda and \
+            ok = x.dtype is dtype and x.shape == shape and x.get_device() == device >= 0 and \
                 (x.is_contiguous() or (name in strided and (x.stride(-1) == 1 or x.shape[-1] == 1 or x.numel() == 0)))
         except AttributeError:
             ok = False
-        if not ok or (device is not None and x.get_device() != device):
+        if not ok:
             _refuse(name, x, shape, dtype, name in strided, device)
-        if device is None:
-            device = x.get_device()
         args.append(x.data_ptr() or None)
     if not isinstance(workspace, torch.Tensor) or workspace.get_device() != device or not workspace.is_contiguous():
         raise MlraError(1, f"workspace has to be a contiguous tensor on cuda:{device}")
     args += (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(device)  # without a Stream object around it
         status = fn(ctypes.byref(dims), *lead, *args, _stream(stream))
     else:
         with torch.cuda.device(device):
