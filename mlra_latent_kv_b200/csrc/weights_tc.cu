@@ -14,15 +14,18 @@
 //     sum over its own registers: no shuffles, no atomics, and the padding to
 //     128 rows is spent on tokens, of which there are plenty, not on heads.
 //   * The query of the current sequence stays in shared memory (147 KB at 128
-//     heads), the cache passes through a ring of 16 KB blocks (128 tokens x 64
-//     dims) that fills the rest: 80 KB in flight at 128 heads, 176 KB at 32.
-//   * A unit is (tile, branch), its scores one of 512 / heads TMEM buffers; the
-//     tile's rotary block comes first and starts every branch's buffer (it is
-//     loaded once), the branch's latent blocks finish it.
-//   * Warps: 0 loads the cache, 1 issues the MMAs, 2 loads the query of the
-//     next sequence as soon as the last MMA of this one is done (the cache
-//     keeps streaming meanwhile), 4-11 exponentiate: two warps per TMEM lane
-//     quarter, half of the heads each.
+//     heads), the cache passes through two rings of 16 KB blocks (128 tokens x
+//     64 dims), latent and rotary, that fill the rest: 80 KB in flight at 128
+//     heads, 208 KB at 32.
+//   * A unit is (tile, branch), its scores one of 512 / heads TMEM buffers.  The
+//     tile's rotary block starts each branch's buffer when its turn comes and
+//     stays (loaded once) until the last branch's, the branch's latent blocks
+//     finish the buffer.  (Started for all branches at once, a tile waits until
+//     the exponentials of the whole tile before are done.)
+//   * Warps: 0 loads the latent, 3 the rotary keys, 1 issues the MMAs, 2 loads
+//     the query of the next sequence as soon as the last MMA of this one is
+//     done (the cache keeps streaming meanwhile), 4-11 exponentiate: two warps
+//     per TMEM lane quarter, half of the heads each.
 //   * CTAs share the tiles evenly, sequences laid end to end, as the decode's
 //     split does.
 //   * Every mbarrier wait is bounded; a CTA that gives up records the site,
@@ -44,7 +47,8 @@ using namespace ptx;
 
 constexpr int kWtTile = 128;        // tokens of a tile: two pages
 constexpr int kWtBlock = 128 * 128;  // 128 tokens x 64 bf16
-constexpr int kWtStages = 12;        // ring blocks at most
+constexpr int kWtStages = 12;        // latent blocks at most
+constexpr int kWtRopes = 2;          // rotary blocks at most
 constexpr int kWtBufs = 16;          // TMEM buffers at most
 constexpr int kWtThreads = 12 * 32;
 constexpr int kWtSmx0 = 4;           // first exponentiating warp
@@ -53,6 +57,7 @@ constexpr int kWtMaxRow = 512;       // n_branch * heads
 
 struct WtBars {
   uint64_t full[kWtStages], empty[kWtStages];
+  uint64_t r_full[kWtRopes], r_empty[kWtRopes];
   uint64_t s_full[kWtBufs], s_free[kWtBufs];
   uint64_t q_full, q_empty, drain;
   alignas(16) float lse[2][kWtMaxRow];  // of the sequence, double-buffered; read four at a time
@@ -75,7 +80,7 @@ struct RingPos {
   }
 };
 
-enum { kWsRing = 40, kWsFull, kWsQEmpty, kWsQFull, kWsFree, kWsScores };
+enum { kWsRing = 40, kWsFull, kWsQEmpty, kWsQFull, kWsFree, kWsScores, kWsRopeRing, kWsRope };
 
 // The tiles of CTA c of G, one after another.
 struct TileCursor {
@@ -127,14 +132,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     weights_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                       const __grid_constant__ CUtensorMap tm_q, const float* __restrict__ lse,
                       const int* __restrict__ page_table, const int* __restrict__ seq_lens, const float* w_in,
-                      float* w_out, int* __restrict__ err, WeightArgs a, int Hp, int stages, int bufs) {
+                      float* w_out, int* __restrict__ err, WeightArgs a, int Hp, int stages, int ropes, int bufs) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nlat = a.d_c / 64, nblk = nlat + 1;  // 64-dim blocks of the latent, and with the rotary one
   const int q_block = Hp * 128;
   uint8_t* sQ = smem;                    // [nblk][Hp rows]
-  uint8_t* sT = smem + nblk * q_block;   // the ring (Hp is a multiple of 16: 1024-byte aligned)
-  WtBars* bars = reinterpret_cast<WtBars*>(sT + stages * kWtBlock);
+  uint8_t* sT = smem + nblk * q_block;   // the rings (Hp is a multiple of 16: 1024-byte aligned)
+  uint8_t* sR = sT + stages * kWtBlock;
+  WtBars* bars = reinterpret_cast<WtBars*>(sR + ropes * kWtBlock);
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int maxL = a.maxp * kPage;
@@ -144,6 +150,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     for (int k = 0; k < stages; ++k) {
       mbar_init(smem_u32(&bars->full[k]), 1);
       mbar_init(smem_u32(&bars->empty[k]), 1);
+    }
+    for (int k = 0; k < ropes; ++k) {
+      mbar_init(smem_u32(&bars->r_full[k]), 1);
+      mbar_init(smem_u32(&bars->r_empty[k]), 1);
     }
     for (int k = 0; k < bufs; ++k) {
       mbar_init(smem_u32(&bars->s_full[k]), 1);
@@ -172,8 +182,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   TileCursor cur(seq_lens, a.B, maxL, blockIdx.x, gridDim.x);
   const long long n = cur.n;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ the cache
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------- the cache: latent blocks, rotary blocks
+    const bool rope = warp == 3;
+    const CUtensorMap* map = rope ? &tm_rope : &tm_lat;
+    uint64_t *full = rope ? bars->r_full : bars->full, *empty = rope ? bars->r_empty : bars->empty;
+    uint8_t* to = rope ? sR : sT;
+    const int size = rope ? ropes : stages, blocks = rope ? 1 : nlat;
     RingPos ring;
     int filled = 0;  // blocks in the ring, up to its size
     bool ok = true;
@@ -193,28 +208,26 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         report_error(err, kErrDeviceCheck, cur.b, (2 * cur.t + lane) * kPage);
         id = 0;
       }
-      for (int k = 0; k < nblk; ++k) {
+      for (int k = 0; k < blocks; ++k) {
         const int s = ring.i;
-        if (filled == stages) {
-          ok = mbar_wait_warp(smem_u32(&bars->empty[s]), ring.round ^ 1u, abort_flag, err, kWsRing);
+        if (filled == size) {
+          ok = mbar_wait_warp(smem_u32(&empty[s]), ring.round ^ 1u, abort_flag, err, rope ? kWsRopeRing : kWsRing);
           if (!ok) break;
         } else {
           ++filled;
         }
-        const uint32_t fb = smem_u32(&bars->full[s]);
+        const uint32_t fb = smem_u32(&full[s]);
         if (lane == 0) mbar_expect_tx(fb, (uint32_t)np * (kWtBlock / 2));
         __syncwarp();
-        if (lane < np)
-          tma_load_2d(smem_u32(sT + s * kWtBlock + lane * (kWtBlock / 2)), k == 0 ? &tm_rope : &tm_lat, fb,
-                      k == 0 ? 0 : 64 * (k - 1), id * kPage);
+        if (lane < np) tma_load_2d(smem_u32(to + s * kWtBlock + lane * (kWtBlock / 2)), map, fb, 64 * k, id * kPage);
         __syncwarp();
-        ring.step(stages);
+        ring.step(size);
       }
       cur = next;
       id = id_next;
     }
     if (!ok)  // what is still on its way; the block that was waited for had landed before
-      for (int k = 0; k < filled; ++k, ring.step(stages)) drain_wait(smem_u32(&bars->full[ring.i]), ring.round ^ 1u);
+      for (int k = 0; k < filled; ++k, ring.step(size)) drain_wait(smem_u32(&full[ring.i]), ring.round ^ 1u);
   } else if (warp == 2) {
     // ------------------------------------------------------------ the query
     uint32_t seg = 0;
@@ -235,14 +248,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const uint32_t idesc = idesc_bf16_f32(128, Hp, false, false);
       const int per = nlat / a.n_branch;  // latent blocks of a branch
       const uint64_t td0 = sdesc_sw128(smem_u32(sT), 16, 1024), qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      RingPos ring, unit;  // the next block; the tile's first score buffer
+      const uint64_t rd0 = sdesc_sw128(smem_u32(sR), 16, 1024);
+      RingPos ring, rope, unit;  // the next latent block, the tile's rotary block, the next score buffer
       bool lap = false;    // every score buffer has been used
       uint32_t seg = 0;
       bool ok = true;
-      // block q of the query against the ring's block, into score buffer `buf`
-      auto product = [&](int q, int buf, bool add) {
-        const uint64_t td = td0 + (uint64_t)(ring.i * (kWtBlock >> 4)), qd = qd0 + (uint64_t)(q * (q_block >> 4));
-        const uint32_t d = tmem + (uint32_t)(buf * stride);
+      // block q of the query against the block at td, into the unit's score buffer
+      auto product = [&](int q, uint64_t td, bool add) {
+        const uint64_t qd = qd0 + (uint64_t)(q * (q_block >> 4));
+        const uint32_t d = tmem + (uint32_t)(unit.i * stride);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           mma_ss(d, td + (uint64_t)(2 * ks), qd + (uint64_t)(2 * ks), idesc, add || ks ? 1u : 0u);
@@ -262,27 +276,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           if (!ok) break;
           ++seg;
         }
-        if (!landed()) break;
-        RingPos u = unit;
-        for (int br = 0; ok && br < a.n_branch; ++br) {  // the rotary part starts every branch
-          if (lap) ok = mbar_wait(smem_u32(&bars->s_free[u.i]), u.round ^ 1u, abort_flag, err, kWsFree);
+        for (int br = 0, k = 0; ok && br < a.n_branch; ++br) {
+          if (lap) ok = mbar_wait(smem_u32(&bars->s_free[unit.i]), unit.round ^ 1u, abort_flag, err, kWsFree);
+          if (ok && br == 0) ok = mbar_wait(smem_u32(&bars->r_full[rope.i]), rope.round, abort_flag, err, kWsRope);
           if (!ok) break;
           tc_fence_after();
-          product(nlat, u.i, false);
-          u.step(bufs);
-          lap = lap || u.i == 0;
-        }
-        if (!ok) break;
-        release();
-        for (int br = 0, k = 0; ok && br < a.n_branch; ++br) {
+          product(nlat, rd0 + (uint64_t)(rope.i * (kWtBlock >> 4)), false);  // the rotary part starts every branch
+          if (br + 1 == a.n_branch) mma_commit(smem_u32(&bars->r_empty[rope.i]));
           for (int e = 0; e < per; ++e, ++k) {
             if (!landed()) break;
-            product(k, unit.i, true);
+            product(k, td0 + (uint64_t)(ring.i * (kWtBlock >> 4)), true);
             if (e + 1 == per) mma_commit(smem_u32(&bars->s_full[unit.i]));
             release();
           }
           unit.step(bufs);
+          lap = lap || unit.i == 0;
         }
+        rope.step(ropes);
         if (ok && cur.last()) mma_commit(smem_u32(&bars->q_empty));
       }
       if (!ok || *abort_flag) {
@@ -399,15 +409,16 @@ cudaError_t launch_weights_tc(const void* q_abs, const float* lse, const void* l
   }
   const int q_bytes = (D / 64) * Hp * 128;
   const int fit = (kWtSmem - 1024 - q_bytes - (int)sizeof(WtBars)) / kWtBlock;
-  const int stages = fit < kWtStages ? fit : kWtStages;
-  if (stages < 2) return cudaErrorInvalidValue;
+  if (fit < 3) return cudaErrorInvalidValue;
+  // a second rotary block where there is room (128 heads: four latent blocks and one)
+  const int ropes = fit < 6 ? 1 : kWtRopes, stages = fit - ropes < kWtStages ? fit - ropes : kWtStages;
   const int stride = (Hp + 31) / 32 * 32;
   const int bufs = 512 / stride < kWtBufs ? 512 / stride : kWtBufs;
-  const int smem = 1024 + q_bytes + stages * kWtBlock + (int)sizeof(WtBars);
+  const int smem = 1024 + q_bytes + (stages + ropes) * kWtBlock + (int)sizeof(WtBars);
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(weights_tc_kernel), smem);
   if (e != cudaSuccess) return e;
   weights_tc_kernel<<<sms, kWtThreads, smem, st>>>(tl, tr, tq, lse, page_table, seq_lens, w_in, w_out, err, a, Hp,
-                                                   stages, bufs);
+                                                   stages, ropes, bufs);
   return cudaGetLastError();
 }
 
