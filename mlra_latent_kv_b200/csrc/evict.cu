@@ -15,6 +15,9 @@
 // and writes both lists, in slot order, beside the shifted weights, table and
 // length.  It is bound by latency: a sequence's weights are read from HBM once
 // and kept in shared memory.  evict_move_kernel copies the rows, bound by HBM.
+// Measured: 64 sequences of 1024 to 32768 tokens that lose half 83 us, 28 of
+// them the selection, then 288 MB at 5.25 TB/s; four of 131072 that lose three
+// quarters 74 us, 30 of them the selection.
 #include <cooperative_groups.h>
 
 #include "host_cache.h"

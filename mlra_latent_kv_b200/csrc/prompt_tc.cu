@@ -37,8 +37,15 @@
 //   * Value rows past a sequence's end are zeroed in shared memory before the
 //     product (a NaN there would get past P = 0); key rows past it are masked.
 //   * The rotation of the queries runs in the kernel before this one, beside
-//     the plan (sequences checked, items sorted by length); its output is
-//     bf16, as the tensor cores want it.
+//     the plan (sequences checked, items sorted by length).
+//   * Rounded to bf16, because the tensor cores take operands of one type: the
+//     rotated queries and P (V is bf16).  The output is within 0.0025 of the
+//     exact one (2-norm), its own rounding to bf16 is 0.0017 of that; statistics
+//     and sums are fp32.
+//   * Measured (calls among others): 128 heads x 4096 tokens 745 to 757 us, 908
+//     to 923 TFLOP/s at the 1545 MHz that the power cap leaves, 640 in a burst;
+//     16 ragged sequences up to 1900 tokens, 32 heads 148 us; four chunks behind
+//     up to 8000 tokens, 32 heads on 8, 265 us.
 //   * Every wait is bounded; a CTA that gives up records the site, lets its
 //     copies and MMAs in flight end and leaves.
 #include <cuda.h>

@@ -5,6 +5,13 @@
 // Bound by HBM: a token is 1152 B (d_c = 512) and 2 * 128 * 576 flops at 128
 // heads, 128 flop/B against the card's 250; four branches take 4 * 128
 // exponentials a token, 70 % of the exponential unit's rate at full bandwidth.
+// Measured (calls among others): 64 sequences of 1024 to 32768 tokens, 32
+// heads: 112 us, 6.2 TB/s, 95 % of the copy bandwidth; 32 x 16384 tokens, four
+// branches of 128 heads: 149 to 161 us under the power cap, 125 in a burst.
+//
+// The tensor core's fp32 sums truncate: a logit is a few units in its last
+// place low in magnitude, a weight within 4e-6.  The log-sum-exp of the decode
+// kernels comes from sums of the same kind.
 //
 // Design (B200):
 //   * The tokens are the rows of the product: S^T[128 tokens, heads] =
@@ -16,7 +23,7 @@
 //   * The query of the current sequence stays in shared memory (147 KB at 128
 //     heads), the cache passes through two rings of 16 KB blocks (128 tokens x
 //     64 dims), latent and rotary, that fill the rest: 80 KB in flight at 128
-//     heads, 208 KB at 32.
+//     heads, 176 KB at 32.
 //   * A unit is (tile, branch), its scores one of 512 / heads TMEM buffers.  The
 //     tile's rotary block starts each branch's buffer when its turn comes and
 //     stays (loaded once) until the last branch's, the branch's latent blocks

@@ -147,6 +147,14 @@ def test_prompt_behind_a_context_and_rows_without_keys(dtype, H, kv, q_lens, k_l
     p.check()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d_h,d_r,d_v", [(512, 64, 32), (512, 64, 100), (40, 6, 300), (512, 64, 512), (5, 2, 3)])
+def test_prompt_other_widths(dtype, d_h, d_r, d_v):
+    p = Prompt(dtype, (70, 1, 150), (170, 90, 150), 2, 1, dims=dict(d_h=d_h, d_r=d_r, d_v=d_v, d_c=64), seed=10)
+    p.call()
+    p.check()
+
+
 @pytest.mark.parametrize("scale", [0.0, 30.0])
 def test_prompt_flat_and_peaked(scale):
     p = Prompt("bf16", (150, 300), (150, 400), 4, 4, scale=scale, seed=2)
@@ -360,6 +368,13 @@ def test_weights_one_sequence_many_workers(dtype, dims, H, nb):
     x.check(before=False)
 
 
+@pytest.mark.parametrize("dtype,dims,H,nb", [("f32", FULL, 3, 2), ("bf16", dict(TINY, d_r=62), 9, 1)])
+def test_weights_more_pages_than_workers(dtype, dims, H, nb):
+    x = Weights(dtype, (20001, 0, 3000, 77), H, nb, dims, seed=7)
+    x.call()
+    x.check()
+
+
 def test_weights_many_sequences_per_worker():
     rng = np.random.default_rng(3)
     x = Weights("bf16", [int(n) for n in rng.integers(0, 300, 400)], 16, 2, FULL, seed=2)
@@ -464,6 +479,17 @@ class Evict:
     ((128, 640, 333), (2, 9, 5), 0), ((4000, 64, 5000), (31, 0, 70), 200)])
 def test_evict(dtype, dims, lens, pages, recent):
     x = Evict(dtype, lens, pages, recent, dims)
+    want = x.expected()
+    x.call()
+    x.check(want)
+
+
+def test_evict_many_sequences():
+    """Warps whose rows lie in several sequences, some of which lose nothing or move nothing."""
+    rng = np.random.default_rng(4)
+    lens = [int(n) for n in rng.integers(0, 700, 500)]
+    x = Evict("bf16", lens, [int(rng.integers(0, max(1, n // 64 + 1))) for n in lens], 0,
+              dict(d_h=32, d_r=8, d_v=32, d_c=32), seed=8, maxp=70)
     want = x.expected()
     x.call()
     x.check(want)
