@@ -44,8 +44,8 @@
 //     and sums are fp32.
 //   * Measured (calls among others): 128 heads x 4096 tokens 745 to 757 us, 908
 //     to 923 TFLOP/s at the 1545 MHz that the power cap leaves, 640 in a burst;
-//     16 ragged sequences up to 1900 tokens, 32 heads 148 us; four chunks behind
-//     up to 8000 tokens, 32 heads on 8, 265 us.
+//     16 ragged sequences up to 1900 tokens, 32 heads 144 us; four chunks behind
+//     up to 8000 tokens, 32 heads on 8, 260 us.
 //   * Every wait is bounded; a CTA that gives up records the site, lets its
 //     copies and MMAs in flight end and leaves.
 #include <cuda.h>
