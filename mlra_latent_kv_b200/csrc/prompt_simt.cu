@@ -159,8 +159,10 @@ __global__ void __launch_bounds__(kPThreads * kG)
       acc[c].z *= corr;
       acc[c].w *= corr;
     }
+    // up to the query's own key: a later token's value may be a NaN or an infinity, which p = 0 would not hide
+    const int own = min(kPk, off + i + 1 - j0);
 #pragma unroll 4
-    for (int j = 0; j < kPk; ++j) {  // keys past the last have p = 0 and values of 0
+    for (int j = 0; j < own; ++j) {  // keys past the last have p = 0 and values of 0
       const float p = sp[r * (kPk + 1) + j];
 #pragma unroll
       for (int c = 0; c < kV; ++c)

@@ -1,0 +1,116 @@
+"""More of the operators around the decode step on the GPU: values that are
+not finite where the mask hides them, many work items per CTA, groups of heads,
+peaked scores, sequences that overlap.
+
+The bounds are those of test_gpu_serving.py, the 64-bit form is torch's own
+matrix product in float64, one (sequence, head) at a time.
+"""
+import math
+
+import pytest
+import torch
+
+from mlra_latent_kv_b200 import abi
+from test_gpu_serving import FULL, TINY, TORCH, U16, U32, Prompt
+
+pytestmark = pytest.mark.gpu
+
+LOG2E = math.log2(math.e)
+
+
+def _prompt(dtype, q_lens, k_lens, H, kv, **kw):
+    return Prompt(dtype, q_lens, k_lens, H, kv, dims=FULL if dtype == "bf16" else TINY, **kw)
+
+
+def _bits(x):
+    return x.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32)
+
+
+def _rotated(x, pos):
+    d = x.shape[-1]
+    ang = pos.double()[:, None] * 10000.0 ** (-torch.arange(0, d, 2, device=x.device, dtype=torch.float64) / d)
+    c, s, out = ang.cos(), ang.sin(), torch.empty_like(x)
+    out[:, 0::2] = x[:, 0::2] * c - x[:, 1::2] * s
+    out[:, 1::2] = x[:, 0::2] * s + x[:, 1::2] * c
+    return out
+
+
+def _exact(p, b, h, v):
+    """(rows, out, its bound, lse, its bound) of one sequence and head in 64 bits, `v` in place of the values."""
+    q0, q1, k0, k1 = (int(cu[b + i]) for cu in (p.cu_q, p.cu_k) for i in (0, 1))
+    lq, lk, g = q1 - q0, k1 - k0, h // (p.H // p.kv)
+    pos = torch.arange(lq, device="cuda") + lk - lq
+    pages = p.table[b, :-(-lk // 64)].long()
+    rope = p.rope_cache[pages].reshape(-1, p.w["d_r"])[:lk].double()
+    qn, kn, val = p.q_nope[q0:q1, h].double(), p.k_nope[k0:k1, g].double(), v[k0:k1, g].double()
+    qr = _rotated(p.q_rope[q0:q1, h].double(), pos)
+    seen = torch.arange(lk, device="cuda")[None] <= pos[:, None]
+    x = (p.scale * (qn @ kn.T + qr @ rope.T)).masked_fill(~seen, -math.inf)
+    lse = torch.logsumexp(x, 1)
+    w = torch.where(seen, (x - lse[:, None]).exp(), 0)
+    out, spread = w @ val, w @ val.abs()
+    rot = p.scale * qr.abs() @ rope.abs().T
+    dot = (rot + p.scale * qn.abs() @ kn.abs().T).masked_fill(~seen, 0).amax(1) if lk else x.sum(1)
+    rot = rot.masked_fill(~seen, 0).amax(1) if lk else dot
+    off = 2 * (p.w["d_h"] + p.w["d_r"] + 4) * U32 * dot
+    if p.dtype == "bf16":
+        off = off + U16 * rot
+    tol = (torch.expm1(2 * off)[:, None] + (2 * lk + 16) * U32) * spread + 1e-30
+    if p.dtype == "bf16":
+        tol = tol * (1 + U16) + U16 * spread * (1 + U16) + U16 * out.abs()
+    lse_tol = off * LOG2E + (lk + 16) * U32 * LOG2E + 4 * U32 * (lse * LOG2E).abs().nan_to_num(posinf=0)
+    return slice(q0, q1), out, tol, lse * LOG2E, lse_tol
+
+
+def _check(p, heads=None, v=None, skip=None):
+    """Compares the outputs of `heads` (all of them) with the 64-bit form; `skip`: outputs that are looked at elsewhere.
+    Returns the median of bound / |output|."""
+    abi.check_status(p.ws)
+    ratio = []
+    for b in range(len(p.cu_q) - 1):
+        for h in range(p.H) if heads is None else heads:
+            rows, out, tol, lse, lse_tol = _exact(p, b, h, p.v if v is None else v)
+            err = (p.out[rows, h].double() - out).abs()
+            ok = err <= tol
+            if skip is not None:
+                ok |= skip[rows, h]
+            assert ok.all(), f"sequence {b}, head {h}: {int((~ok).sum())} outputs, {(err / tol).max():.2f} of the bound"
+            got, none = p.lse[rows, h].double(), lse.isneginf()
+            assert got[none].isneginf().all() and ((got - lse).abs() <= lse_tol)[~none].all()
+            ratio.append((tol / out.abs())[out != 0].flatten())
+    assert p.out[int(p.cu_q[-1]):].isnan().all() and p.lse[int(p.cu_q[-1]):].isnan().all()
+    return torch.cat(ratio).median().item()
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype,H,kv", [("f32", 4, 4), ("f32", 6, 2)])
+def test_prompt_values_of_later_tokens_do_not_reach_a_query(dtype, H, kv, bad):
+    """A value that is not finite is the output of the queries that see it, in its own column; nothing else changes."""
+    q_lens, k_lens = (300, 5, 140), (300, 700, 200)
+    p = _prompt(dtype, q_lens, k_lens, H, kv, seed=20)
+    clean, hit = p.v.clone(), torch.zeros_like(p.out, dtype=torch.bool)
+    # sequence, kv head, key, column
+    for b, g, j, c in ((0, 0, 211, 3), (0, kv - 1, 90, 17), (1, 0, 698, 0), (2, kv - 1, 199, 31), (2, 0, 61, 8)):
+        p.v[int(p.cu_k[b]) + j, g, c] = bad
+        first = max(0, j - (k_lens[b] - q_lens[b]))  # the first query that sees key j
+        hit[int(p.cu_q[b]) + first:int(p.cu_q[b + 1]), g * (H // kv):(g + 1) * (H // kv), c] = True
+    p.call()
+    _check(p, v=clean, skip=hit)
+    torch.testing.assert_close(p.out[hit].float(), torch.full_like(p.out[hit].float(), bad), equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_keys_of_later_tokens_do_not_reach_a_query(dtype):
+    p = _prompt(dtype, (200, 90), (260, 90), 4, 2, seed=21)
+    p.call()
+    want, want_lse = p.out.clone(), p.lse.clone()
+    p.k_nope[230] = float("nan")  # seen from query 170 of the first sequence on
+    p.k_nope[260 + 64] = float("inf")
+    p.rope_cache[p.table[1, 1].long(), 20] = float("nan")  # key 84 of the second
+    p.call()
+    for rows in (slice(0, 170), slice(200, 264)):
+        assert torch.equal(_bits(p.out[rows]), _bits(want[rows])) and torch.equal(p.lse[rows], want_lse[rows])
+    assert p.out[170:200].isnan().all() and p.out[284:290].isnan().all()
