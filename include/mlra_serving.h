@@ -51,7 +51,9 @@ extern "C" {
  *
  * Rows of out and lse outside every [cu_q[b], cu_q[b+1]) are not touched.
  * What lies behind a sequence's last key (the next sequence's rows, unused
- * slots of its last page) does not reach its output, NaN included.
+ * slots of its last page) does not reach its output, and what lies behind a
+ * query's last key does not reach that query's, NaN and infinities included
+ * (a NaN or an infinity in v costs the queries before it a slower pass).
  *
  *   q_nope [total_q, H, d_h]   q_rope [total_q, H, d_r] (un-rotated)
  *   k_nope [total_k, kv_heads, d_h]   v [total_k, kv_heads, d_v]

@@ -36,6 +36,7 @@
 //     masked step took 3600 cycles more, now 600).
 //   * Value rows past a sequence's end are zeroed in shared memory before the
 //     product (a NaN there would get past P = 0); key rows past it are masked.
+//     A NaN or an infinity of a later token of the sequence: see rows_again.
 //   * The rotation of the queries runs in the kernel before this one, beside
 //     the plan (sequences checked, items sorted by length).
 //   * Rounded to bf16, because the tensor cores take operands of one type: the
@@ -88,6 +89,7 @@ struct PromptBars {
   uint64_t turn[2];     // the other tile has issued its step
   uint64_t drain[2];
   PromptItem item[2];
+  int odd;              // the last of this CTA's items with rows to be taken again, -1 for none
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (s_rows > (unsigned long long)a.total_q) {  // sequences that overlap: the list has no room for them
       if (threadIdx.x == 0) {
         report_error(err, kErrDeviceCheck, a.B, a.total_q);
-        counts[0] = counts[1] = 0;
+        counts[0] = counts[1] = counts[2] = 0;
       }
       return;
     }
@@ -161,6 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       if (threadIdx.x == kPlanThreads - 1) {
         counts[0] = before + incl;  // entries of the list
         counts[1] = 0;              // the next item
+        counts[2] = 0;              // items with values that are not finite
       }
     }
     __syncthreads();
@@ -228,6 +231,148 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ---------------------------------------------------------------------------
+// Values that are not finite.  A tile's last steps hold keys past a row's own,
+// with P = 0 there, and 0 times a NaN or an infinity is a NaN.  Rows that have
+// such a value behind their last key are therefore taken again, over their own
+// keys alone.  Warp 2, which has the least to do, looks at those keys' values
+// while they lie in shared memory and chains their items; the warps other than
+// the softmax's go through the chain behind the CTA's last item, a row each, a
+// lane per key for the scores, four columns a lane for the values.
+//
+// Taken in turns with the kernel that did not look, 128 heads x 4096 tokens
+// 708-744 -> 717-751 us, the ragged batch 131-136 -> 133-140, grouped chunks
+// 247-250 -> 249-254.  (In the epilogue of the softmax warps it cost 3 to 8 %, for
+// the compiler then spilled in their loop; in a kernel of its own behind this one
+// the second part took 2 to 3 us.)  Rows are taken again in short loops that are
+// not unrolled: one token of NaN in all of 128 heads x 4096 tokens takes 51 ms.
+// ---------------------------------------------------------------------------
+struct PromptRows {
+  const __nv_bfloat16 *q_nope, *q_rot, *k_nope, *v, *rope_cache;
+  __nv_bfloat16* out;
+  const int *cu_q, *cu_k, *page_table;
+  int4* odd;  // {sequence, first token, first head, the CTA's one before or -1} of items
+  int pack;
+  PromptArgs a;
+};
+
+// The item of an entry of `odd`.
+__device__ __forceinline__ PromptItem prompt_item(int4 e, const int* cu_q, const int* cu_k, const PromptArgs& a,
+                                                  int pack) {
+  const PromptSeq s = prompt_seq(cu_q, cu_k, e.x, a, nullptr);
+  PromptItem it;
+  it.live = 1;
+  it.b = e.x;
+  it.head0 = e.z;
+  it.kvh = e.z / (a.H / a.kv_heads);
+  it.tok0 = e.y;
+  it.Lq = s.Lq;
+  it.Lk = s.Lk;
+  it.q0 = s.q0;
+  it.k0 = s.k0;
+  it.n[0] = key_tiles(s, it.tok0, 128 / pack);
+  it.n[1] = key_tiles(s, it.tok0 + 128 / pack, 128 / pack);
+  return it;
+}
+
+// The first key of step j, counted from the step's own first, that one of the item's rows in it does not see.
+__device__ __forceinline__ int cut_key(const PromptItem& it, int j, int TT) {
+  const int own = it.Lk - it.Lq + it.tok0 + (j < it.n[0] ? 0 : TT);  // of the first row that has the step
+  return max(0, own + 1 - 128 * j);
+}
+
+// z + the values times zero: a NaN once one of them is not finite.
+__device__ __forceinline__ void add_zeros(__nv_bfloat162& z, uint4 x) {
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&x.x);
+  z = __hadd2(z, __hfma2(p[0], zero, __hfma2(p[1], zero, __hfma2(p[2], zero, __hmul2(p[3], zero)))));
+}
+__device__ __forceinline__ bool is_odd(__nv_bfloat162 z) { return __hisnan(z.x) || __hisnan(z.y); }
+
+__device__ __forceinline__ bool all_nan(uint2 y) {
+  return (y.x & 0x7fffu) > 0x7f80u && (y.x & 0x7fff0000u) > 0x7f800000u && (y.y & 0x7fffu) > 0x7f80u &&
+         (y.y & 0x7fff0000u) > 0x7f800000u;
+}
+
+// s + the sum of the products of eight pairs.
+__device__ __forceinline__ float dot8(uint4 x, uint4 y, float s) {
+  const uint32_t *p = &x.x, *q = &y.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(p[i] << 16), __uint_as_float(q[i] << 16), s);
+    s = fmaf(__uint_as_float(p[i] & 0xffff0000u), __uint_as_float(q[i] & 0xffff0000u), s);
+  }
+  return s;
+}
+
+// The rows of an item that have to be taken again: rows `first`, first + 4, .. of them.
+__device__ __forceinline__ void rows_again(const PromptItem& it, int first, const PromptRows& rows) {
+  const PromptArgs& a = rows.a;
+  const int pack = rows.pack, lane = threadIdx.x & 31, TT = 128 / pack;
+  const __nv_bfloat16* vals = rows.v + (size_t)it.k0 * a.v_s[0] + (size_t)it.kvh * a.v_s[1] + 4 * lane;
+  auto value = [&](int j) { return __ldg(reinterpret_cast<const uint2*>(vals + (size_t)j * a.v_s[0])); };
+  for (int x = 0; x < 2; ++x) {
+    const int tok0 = it.tok0 + x * TT, toks = min(TT, it.Lq - tok0);  // the tile's tokens
+    const int own = it.Lk - it.Lq + tok0, end = min(it.Lk, 128 * it.n[x]);
+    // of the keys behind the first row's own: the last whose value is not finite, the first whose value is all NaN
+    int last = -1, all = end;
+    for (int j = max(0, own + 1); j < end && all == end; ++j) {
+      const uint2 y = value(j);
+      __nv_bfloat162 z = __float2bfloat162_rn(0.f);
+      add_zeros(z, make_uint4(y.x, y.y, 0u, 0u));
+      if (__any_sync(0xffffffffu, is_odd(z))) last = j;
+      if (__all_sync(0xffffffffu, all_nan(y))) all = j;
+    }
+    // tokens whose own key is before the last (those that see the value that is all NaN are NaN as they are)
+    const int stop = min(toks, last - own);
+    for (int r = max(0, -own) * pack + first; r < stop * pack; r += 4) {  // those before have no key
+      const int tok = it.q0 + tok0 + r / pack, head = it.head0 + r % pack, lim = own + r / pack;
+      const uint4* qn = reinterpret_cast<const uint4*>(rows.q_nope + (size_t)tok * a.q_nope_s[0] +
+                                                       (size_t)head * a.q_nope_s[1]);
+      const uint4* qr = reinterpret_cast<const uint4*>(rows.q_rot + ((size_t)tok * a.H + head) * 64);
+      float o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+      for (int j0 = 0; j0 <= lim; j0 += 32) {
+        const int j = min(j0 + lane, lim);
+        const uint4* kn = reinterpret_cast<const uint4*>(rows.k_nope + (size_t)(it.k0 + j) * a.k_nope_s[0] +
+                                                         (size_t)it.kvh * a.k_nope_s[1]);
+        int id = __ldg(rows.page_table + (size_t)it.b * a.maxp + j / kPage);
+        if (id < 0 || id >= a.num_pages) id = 0;  // reported when its step was loaded
+        const uint4* kr = reinterpret_cast<const uint4*>(rows.rope_cache + ((size_t)id * kPage + j % kPage) * 64);
+        float s = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 16; ++c) s = dot8(__ldg(qn + c), __ldg(kn + c), s);
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) s = dot8(qr[c], __ldg(kr + c), s);
+        s = j0 + lane <= lim ? s * a.scale_log2 : -INFINITY;
+        float top = s;
+#pragma unroll
+        for (int i = 16; i >= 1; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+        top = fmaxf(top, m);
+        const float ref = top == -INFINITY ? 0.f : top, corr = ex2(m - ref), p = ex2(s - ref);
+        m = top;
+        l = l * corr + warp_sum(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] *= corr;
+#pragma unroll 1
+        for (int u = 0; u < 32; ++u) {
+          if (j0 + u > lim) break;
+          const float pu = __shfl_sync(0xffffffffu, p, u);
+          const uint2 y = value(j0 + u);
+          o[0] = fmaf(pu, __uint_as_float(y.x << 16), o[0]);
+          o[1] = fmaf(pu, __uint_as_float(y.x & 0xffff0000u), o[1]);
+          o[2] = fmaf(pu, __uint_as_float(y.y << 16), o[2]);
+          o[3] = fmaf(pu, __uint_as_float(y.y & 0xffff0000u), o[3]);
+        }
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
+      *reinterpret_cast<uint2*>(rows.out + ((size_t)tok * a.H + head) * 128 + 4 * lane) =
+          make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // The attention.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPtThreads, 1)
@@ -236,7 +381,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                      const __grid_constant__ CUtensorMap tm_rope, const int* __restrict__ cu_q,
                      const int* __restrict__ cu_k, const int* __restrict__ page_table, const int2* __restrict__ list,
                      int* counts, __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int* __restrict__ err,
-                     PromptArgs a, int pack, int unit_group) {
+                     PromptArgs a, int pack, int unit_group, const __grid_constant__ PromptRows rows) {
   constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);  // V read MN-major
   extern __shared__ uint8_t smem_raw[];
@@ -267,6 +412,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       mbar_init(smem_u32(&bars->item_empty[x]), 11);  // the MMA threads, warp 2 and eight softmax warps
     }
     bars->abort_flag = 0;
+    bars->odd = -1;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -431,6 +577,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
       if (lse && mine) lse[at] = l == 0.f ? -INFINITY : m * sc + log2f(l);
     }
+    asm volatile("bar.arrive 1, %0;" ::"n"(kPtThreads) : "memory");  // the outputs are written
   } else {
     setmaxnreg_dec<kPtRegsAux>();
   if (warp == 0) {
@@ -704,19 +851,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    // ------------------------------------ value rows past a sequence's end
+    // ------------- value rows past a sequence's end, values that are not finite
     uint32_t t = 0, ends = 0;
     bool ok = true;
     PromptItem it;
     for (uint32_t i = 0; ok && take(i, &it) && it.live; ++i) {
       const int n = max(it.n[0], it.n[1]);
+      __nv_bfloat162 z = __float2bfloat162_rn(0.f);
       for (int j = 0; ok && j < n; ++j, ++t) {
-        const int rows = it.Lk - 128 * j;  // of the value tile, inside the sequence
+        const int left = it.Lk - 128 * j;  // of the value tile, inside the sequence
         ok = mbar_wait_warp(smem_u32(&bars->v_full[t & 1]), (t >> 1) & 1, abort_flag, err, kPsV);
         if (!ok) break;
-        if (rows < 128) {  // the sequence's last value tile
+        if (left < 128) {  // the sequence's last value tile
           for (int half = 0; half < 2; ++half) {
-            const int r0 = min(64, max(0, rows - 64 * half)), nz = (64 - r0) * 8;  // 16-byte pieces of 64 dims
+            const int r0 = min(64, max(0, left - 64 * half)), nz = (64 - r0) * 8;  // 16-byte pieces of 64 dims
             uint8_t* to = sR + ((5 * t + 3 + half) % kPtRing) * kPtBlock + r0 * 128;
             for (int e = lane; e < nz; e += 32)
 #pragma unroll
@@ -728,10 +876,32 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           if (lane == 0) mbar_arrive(smem_u32(&bars->v_fixed[ends & 1]));
           ++ends;
         }
+        const int key0 = cut_key(it, j, TT);
+        for (int half = key0 >> 6; half < 2; ++half) {
+          const int r0 = max(0, key0 - 64 * half);
+          const uint8_t* from = sR + ((5 * t + 3 + half) % kPtRing) * kPtBlock + r0 * 128;
+#pragma unroll 2
+          for (int e = lane; e < (64 - r0) * 8; e += 32)
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+              add_zeros(z, *reinterpret_cast<const uint4*>(from + d * (kPtBlock / 2) + e * 16));
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->v_empty[t & 1]));
       }
+      if (__any_sync(0xffffffffu, is_odd(z)) && lane == 0) {
+        const int at = atomicAdd(counts + 2, 1);
+        rows.odd[at] = make_int4(it.b, it.tok0, it.head0, bars->odd);
+        bars->odd = at;
+      }
     }
+  }
+  // the outputs are written, all values have been seen
+  named_barrier(1, kPtThreads);
+  for (int e = *abort_flag ? -1 : *reinterpret_cast<volatile int*>(&bars->odd); e >= 0;) {
+    const int4 o = __ldcg(rows.odd + e);
+    rows_again(prompt_item(o, rows.cu_q, rows.cu_k, rows.a, rows.pack), warp, rows);
+    e = o.w;
   }
   }
   tc_fence_before();
@@ -749,17 +919,27 @@ int heads_packed(int H, int kv_heads) {
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 long long list_entries(const PromptArgs& a, int pack) { return ((long long)a.total_q * pack + 255) / 256 + a.B; }
 
+// error record | item counts | list of tile pairs | items to be taken again in part | rotated queries
+struct PromptLayout {
+  size_t list, odd, q_rot, total;
+};
+PromptLayout prompt_layout(const PromptArgs& a, int pack) {
+  const size_t entries = (size_t)list_entries(a, pack);
+  PromptLayout l;
+  l.list = 512;
+  l.odd = round_up(l.list + entries * sizeof(int2), 256);
+  l.q_rot = round_up(l.odd + entries * (a.H / pack) * sizeof(int4), 256);
+  l.total = round_up(l.q_rot + (size_t)a.total_q * a.H * 64 * 2, 256);
+  return l;
+}
+
 }  // namespace
 
 bool prompt_tc_supported(int dtype, int d_h, int d_r, int d_v) {
   return dtype == MLRA_BF16 && d_h == 128 && d_r == 64 && d_v == 128;
 }
 
-// error record | item counts | list of tile pairs | rotated queries
-size_t prompt_tc_workspace(const PromptArgs& a) {
-  const size_t list = round_up((size_t)list_entries(a, heads_packed(a.H, a.kv_heads)) * sizeof(int2), 256);
-  return 512 + list + round_up((size_t)a.total_q * a.H * 64 * 2, 256);
-}
+size_t prompt_tc_workspace(const PromptArgs& a) { return prompt_layout(a, heads_packed(a.H, a.kv_heads)).total; }
 
 cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* cu_q, const void* k_nope,
                              const void* v, const int* cu_k, const void* rope_cache, const int* page_table, void* out,
@@ -769,9 +949,11 @@ cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* 
   char* ws = static_cast<char*>(workspace);
   int* err = reinterpret_cast<int*>(ws);
   int* counts = reinterpret_cast<int*>(ws + 256);
-  int2* list = reinterpret_cast<int2*>(ws + 512);
+  const PromptLayout at = prompt_layout(a, pack);
+  int2* list = reinterpret_cast<int2*>(ws + at.list);
+  int4* odd = reinterpret_cast<int4*>(ws + at.odd);
   const long long entries = list_entries(a, pack);
-  __nv_bfloat16* q_rot = reinterpret_cast<__nv_bfloat16*>(ws + 512 + round_up((size_t)entries * sizeof(int2), 256));
+  __nv_bfloat16* q_rot = reinterpret_cast<__nv_bfloat16*>(ws + at.q_rot);
 
   // packed [tokens][heads][width]; an axis of one element takes any valid stride
   auto packed = [&](CUtensorMap* m, const void* p, int width, int heads, int rows, const long long* s, int box_heads,
@@ -814,6 +996,9 @@ cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* 
     return cudaFuncGetAttributes(&f, prompt_tc_kernel) == cudaSuccess ? f.numRegs : 0;
   }();
   if (regs != kPtRegs) return cudaErrorInvalidConfiguration;
+  const PromptRows rows{static_cast<const __nv_bfloat16*>(q_nope), q_rot, static_cast<const __nv_bfloat16*>(k_nope),
+                        static_cast<const __nv_bfloat16*>(v), static_cast<const __nv_bfloat16*>(rope_cache),
+                        static_cast<__nv_bfloat16*>(out), cu_q, cu_k, page_table, odd, pack, a};
   const int smem = 1024 + kPtSmem + (int)sizeof(PromptBars);
   e = ensure_smem(reinterpret_cast<const void*>(prompt_tc_kernel), smem);
   if (e != cudaSuccess) return e;
@@ -829,7 +1014,7 @@ cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* 
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, prompt_tc_kernel, tqn, tqr, tk, tv, tr, cu_q, cu_k, page_table,
                             static_cast<const int2*>(list), counts, static_cast<__nv_bfloat16*>(out), lse, err, a, pack,
-                            (int)group);
+                            (int)group, rows);
 }
 
 }  // namespace mlra

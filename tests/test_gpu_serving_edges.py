@@ -86,7 +86,7 @@ def _check(p, heads=None, v=None, skip=None):
 # values that are not finite
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
-@pytest.mark.parametrize("dtype,H,kv", [("f32", 4, 4), ("f32", 6, 2)])
+@pytest.mark.parametrize("dtype,H,kv", [("f32", 4, 4), ("f32", 6, 2), ("bf16", 4, 4), ("bf16", 16, 2), ("bf16", 128, 1)])
 def test_prompt_values_of_later_tokens_do_not_reach_a_query(dtype, H, kv, bad):
     """A value that is not finite is the output of the queries that see it, in its own column; nothing else changes."""
     q_lens, k_lens = (300, 5, 140), (300, 700, 200)
@@ -100,6 +100,19 @@ def test_prompt_values_of_later_tokens_do_not_reach_a_query(dtype, H, kv, bad):
     p.call()
     _check(p, v=clean, skip=hit)
     torch.testing.assert_close(p.out[hit].float(), torch.full_like(p.out[hit].float(), bad), equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype,H,kv", [("f32", 4, 2), ("bf16", 4, 4), ("bf16", 16, 2)])
+def test_prompt_tokens_whose_values_are_all_nan(dtype, H, kv):
+    """The tokens behind the first of them, too: a row that is NaN as it is, and rows before it with a second one."""
+    p = _prompt(dtype, (400, 130), (400, 390), H, kv, seed=22)
+    clean, hit = p.v.clone(), torch.zeros_like(p.out, dtype=torch.bool)
+    p.v[[150, 160, 399, 400 + 300]] = float("nan")
+    p.v[140, 0, 5] = float("inf")
+    hit[150:400], hit[400 + 40:400 + 130], hit[140:150, :H // kv, 5] = True, True, True  # 300 - (390 - 130) = 40
+    p.call()
+    _check(p, v=clean, skip=hit)
+    assert p.out[150:400].isnan().all() and p.out[440:530].isnan().all() and p.out[140:150, :H // kv, 5].isposinf().all()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
