@@ -51,6 +51,8 @@
 //     copies and MMAs in flight end and leaves.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "host_cache.h"
 #include "launch.h"
 #include "serving.h"
@@ -939,6 +941,17 @@ bool prompt_tc_supported(int dtype, int d_h, int d_r, int d_v) {
   return dtype == MLRA_BF16 && d_h == 128 && d_r == 64 && d_v == 128;
 }
 
+cudaError_t prompt_tc_registers(int* regs, int* want) {
+  static std::atomic<int> known{0};  // of the code, the same on every device; a failed query is not kept
+  *want = kPtRegs;
+  *regs = known.load(std::memory_order_relaxed);
+  if (*regs != 0) return cudaSuccess;
+  cudaFuncAttributes f;
+  const cudaError_t e = cudaFuncGetAttributes(&f, prompt_tc_kernel);
+  if (e == cudaSuccess) known.store(*regs = f.numRegs, std::memory_order_relaxed);
+  return e;
+}
+
 size_t prompt_tc_workspace(const PromptArgs& a) { return prompt_layout(a, heads_packed(a.H, a.kv_heads)).total; }
 
 cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* cu_q, const void* k_nope,
@@ -990,12 +1003,6 @@ cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* 
   group = group < 1 ? 1 : (group > units ? units : group);
   const long long groups = (units + group - 1) / group;
   group = (units + groups - 1) / groups;
-  // what the roles are dealt has to be there: the kernel's registers at launch
-  static const int regs = [] {
-    cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, prompt_tc_kernel) == cudaSuccess ? f.numRegs : 0;
-  }();
-  if (regs != kPtRegs) return cudaErrorInvalidConfiguration;
   const PromptRows rows{static_cast<const __nv_bfloat16*>(q_nope), q_rot, static_cast<const __nv_bfloat16*>(k_nope),
                         static_cast<const __nv_bfloat16*>(v), static_cast<const __nv_bfloat16*>(rope_cache),
                         static_cast<__nv_bfloat16*>(out), cu_q, cu_k, page_table, odd, pack, a};

@@ -66,6 +66,8 @@ __device__ __forceinline__ PromptSeq prompt_seq(const int* cu_q, const int* cu_k
 }
 
 bool prompt_tc_supported(int dtype, int d_h, int d_r, int d_v);
+// Registers of a thread of the kernel as it was compiled, and the number that it needs (see prompt_path.h).
+cudaError_t prompt_tc_registers(int* regs, int* want);
 size_t prompt_tc_workspace(const PromptArgs& a);
 cudaError_t launch_prompt_tc(const void* q_nope, const void* q_rope, const int* cu_q, const void* k_nope,
                              const void* v, const int* cu_k, const void* rope_cache, const int* page_table, void* out,

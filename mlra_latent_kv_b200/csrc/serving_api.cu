@@ -8,6 +8,7 @@
 
 #include "gemm_tc.h"
 #include "launch.h"
+#include "prompt_path.h"
 #include "serving.h"
 
 namespace mlra {
@@ -205,13 +206,20 @@ mlra_status mla_prompt(const mlra_dims* dims, const mla_prompt_shape* shape, con
     const PromptArgs a = prompt_args(d, s);
     if (st == MLRA_OK) st = check_workspace(workspace, workspace_bytes, prompt_workspace(d, a));
     if (st != MLRA_OK) return st;
-    const bool tc_ok = prompt_tc_supported(d->dtype, d->d_h, d->d_r, d->d_v) &&
-                       prompt_aligned(a, q_nope, q_rope, k_nope, v);
-    if (d->kernel == MLRA_KERNEL_TC && !tc_ok)
+    const bool fits = prompt_tc_supported(d->dtype, d->d_h, d->d_r, d->d_v) &&
+                      prompt_aligned(a, q_nope, q_rope, k_nope, v);
+    int regs = 0, want = 0;
+    if (fits && d->kernel != MLRA_KERNEL_SIMT)
+      if (cudaError_t err = prompt_tc_registers(&regs, &want))
+        return bad(MLRA_ERR_CUDA, "query of the prompt kernel: %s", cudaGetErrorString(err));
+    const PromptPath path = prompt_path(static_cast<mlra_kernel>(d->kernel), fits, regs, want);
+    if (path == PromptPath::kNoShape)
       return bad(MLRA_ERR_UNSUPPORTED,
                  "the tcgen05 prompt kernel needs bf16, d_h=128, d_r=64, d_v=128 and 16-byte aligned rows");
+    if (path == PromptPath::kNoRegisters)
+      return bad(MLRA_ERR_UNSUPPORTED, "the tcgen05 prompt kernel was compiled to %d registers, not %d", regs, want);
     const RopeTable tab = internal_rope_table(d);
-    if (tc_ok && d->kernel != MLRA_KERNEL_SIMT) {
+    if (path == PromptPath::kTc) {
       const int sms = device_sms();
       if (sms == 0) return MLRA_ERR_CUDA;
       return launched(launch_prompt_tc(q_nope, q_rope, cu_q, k_nope, v, cu_k, rope_cache, page_table, out, lse,

@@ -1,0 +1,43 @@
+"""Host-side rules and refusals of the operators around the decode step that
+need no GPU, beyond those of test_serving_cpu.py."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from mlra_latent_kv_b200 import abi, build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return abi.lib()
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_prompt_takes_the_cuda_core_kernel_where_the_other_was_compiled_otherwise(tmp_path):
+    src, exe = tmp_path / "path.cc", str(tmp_path / "path")
+    src.write_text("""
+#include "prompt_path.h"
+using namespace mlra;
+#define IS(kernel, fits, regs, path) if (prompt_path(kernel, fits, regs, 168) != PromptPath::path) return __LINE__;
+int main() {
+  IS(MLRA_KERNEL_AUTO, true, 168, kTc)
+  IS(MLRA_KERNEL_TC, true, 168, kTc)
+  IS(MLRA_KERNEL_AUTO, true, 160, kSimt)
+  IS(MLRA_KERNEL_AUTO, true, 255, kSimt)
+  IS(MLRA_KERNEL_TC, true, 160, kNoRegisters)
+  IS(MLRA_KERNEL_AUTO, false, 0, kSimt)
+  IS(MLRA_KERNEL_TC, false, 0, kNoShape)
+  IS(MLRA_KERNEL_SIMT, true, 168, kSimt)
+  IS(MLRA_KERNEL_SIMT, false, 0, kSimt)
+}
+""")
+    r = subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", "/usr/local/cuda/include", "-I",
+                        os.path.join(ROOT, "mlra_latent_kv_b200", "csrc"), str(src), "-o", exe], capture_output=True,
+                       text=True)
+    assert r.returncode == 0, r.stderr
+    assert subprocess.run([exe]).returncode == 0
