@@ -11,6 +11,7 @@ one is given).
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -328,6 +329,14 @@ def _run(fn, dims, stream, workspace, tensors, lead=(), strided=()):
         raise MlraError(status, last_error())
 
 
+def _int32(name, x) -> int:
+    """x as an int of the library (ctypes would cut a larger one off)."""
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise MlraError(1, f"{name}={x} is out of range")
+    return x
+
+
 def _prompt_shape(q_nope, q_rope, k_nope, v) -> PromptShape:
     s = PromptShape(k_nope.shape[1], q_nope.shape[0], k_nope.shape[0])
     for field, x in ((s.q_nope_stride, q_nope), (s.q_rope_stride, q_rope), (s.k_nope_stride, k_nope), (s.v_stride, v)):
@@ -337,7 +346,8 @@ def _prompt_shape(q_nope, q_rope, k_nope, v) -> PromptShape:
 
 def prompt_workspace_bytes(dims: Dims, total_q: int, total_k: int, kv_heads: int) -> int:
     """Bytes of workspace mla_prompt needs for that many packed rows and kv heads, whatever their strides."""
-    s = PromptShape(kv_heads, total_q, total_k)
+    total_q, total_k = _int32("total_q", total_q), _int32("total_k", total_k)
+    s = PromptShape(_int32("kv_heads", kv_heads), total_q, total_k)
     for name, heads, width in (("q_nope_stride", dims.H, dims.d_h), ("q_rope_stride", dims.H, dims.d_r),
                                ("k_nope_stride", kv_heads, dims.d_h), ("v_stride", kv_heads, dims.d_v)):
         getattr(s, name)[:] = (heads * width, width)
@@ -401,6 +411,7 @@ def latent_evict(dims, recent, evict_pages, weights, page_table, seq_lens, laten
                  page_table_out, seq_lens_out, workspace, stream=None):
     """Frees evict_pages[b] pages of each sequence: the tokens with the least weight leave, but for the last
     ``recent`` (see include/mlra_serving.h)."""
+    recent = _int32("recent", recent)
     B, pages = dims.B, dims.max_pages_per_seq
     ty, pool = _types(), (dims.num_pages, dims.page_size)
     e, i32, f32, slots = ty[dims.dtype], ty["i32"], ty["f32"], (B, pages * dims.page_size)
@@ -409,7 +420,7 @@ def latent_evict(dims, recent, evict_pages, weights, page_table, seq_lens, laten
           ("page_table", page_table, (B, pages), i32), ("seq_lens", seq_lens, (B,), i32),
           ("latent_cache", latent_cache, (*pool, dims.d_c), e), ("rope_cache", rope_cache, (*pool, dims.d_r), e),
           ("weights_out", weights_out, slots, f32), ("page_table_out", page_table_out, (B, pages), i32),
-          ("seq_lens_out", seq_lens_out, (B,), i32)), lead=(int(recent),))
+          ("seq_lens_out", seq_lens_out, (B,), i32)), lead=(recent,))
 
 
 def check_status(workspace, stream=None) -> None:

@@ -41,3 +41,22 @@ int main() {
                        text=True)
     assert r.returncode == 0, r.stderr
     assert subprocess.run([exe]).returncode == 0
+
+
+def _dims(**kw):
+    return abi.make_dims(**(dict(B=2, H=8, d_h=128, d_v=128, d_c=512, d_r=64, max_pages_per_seq=8, num_pages=32) | kw))
+
+
+def test_binding_refuses_numbers_that_do_not_fit(L):
+    """2^32 + 5 would be 5 in the library's 32 bits."""
+    d = _dims()
+    need = abi.prompt_workspace_bytes(d, 100, 100, 8)
+    for sizes in ((2 ** 32 + 100, 100, 8), (100, 2 ** 32 + 100, 8), (100, 100, 2 ** 32 + 8), (-2 ** 32 + 100, 100, 8)):
+        with pytest.raises(abi.MlraError, match="out of range"):
+            abi.prompt_workspace_bytes(d, *sizes)
+    assert abi.prompt_workspace_bytes(d, 100, 100, 8) == need
+    for recent in (2 ** 32 + 5, 2 ** 31, -2 ** 32):
+        with pytest.raises(abi.MlraError, match="recent"):
+            abi.latent_evict(d, recent, *[None] * 10)
+    with pytest.raises(TypeError):  # not a whole number
+        abi.latent_evict(d, 16.5, *[None] * 10)
