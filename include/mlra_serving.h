@@ -19,6 +19,10 @@
  * the calling thread's current device, where all buffers lie.  A workspace
  * serves one call at a time: two calls (or two captured graphs) that may run
  * at the same time need one each.
+ *
+ * Overlap: an output, the workspace among them, shares no byte with an input or
+ * another output (MLRA_ERR_INVALID_ARG), but for mlra_attention_weights in
+ * place.  A strided input counts from its first element to its last.
  */
 #ifndef MLRA_SERVING_H_
 #define MLRA_SERVING_H_
@@ -146,8 +150,7 @@ MLRA_SERVING_API mlra_status mlra_attention_weights(const mlra_dims* dims, const
  *     entries, -1 behind it; entries [0, n) of the old row are the pages that
  *     are free now
  *   seq_lens_out [B] = seq_lens[b] - 64 n
- * Outputs may not overlap inputs.  Decode with page_table_out and
- * seq_lens_out.  Positions do not change: q_pos stays the token's position,
+ * Decode with page_table_out and seq_lens_out.  Positions do not change: q_pos stays the token's position,
  * and latent_append, which finds a token's slot by its position, keeps taking
  * a table indexed by absolute page (the table from before the first eviction,
  * extended by new pages at both tables' ends).

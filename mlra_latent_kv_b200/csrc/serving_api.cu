@@ -110,6 +110,27 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// Outputs (the workspace is one) may share no byte with an input or with one another; an absent buffer has no bytes.
+struct Span {
+  const void* p;
+  size_t n;
+};
+template <int kIn, int kOut>
+mlra_status check_overlap(const Span (&in)[kIn], const Span (&outs)[kOut]) {
+  auto meet = [](const Span& a, const Span& b) { return a.p && b.p && a.n && b.n && overlap(a.p, a.n, b.p, b.n); };
+  for (int o = 0; o < kOut; ++o) {
+    for (const Span& i : in)
+      if (meet(i, outs[o])) return bad(MLRA_ERR_INVALID_ARG, "an output overlaps an input");
+    for (int q = 0; q < o; ++q)
+      if (meet(outs[q], outs[o])) return bad(MLRA_ERR_INVALID_ARG, "two outputs overlap");
+  }
+  return MLRA_OK;
+}
+
+size_t dtype_bytes(const mlra_dims* d) { return d->dtype == MLRA_BF16 ? 2 : 4; }
+size_t pool_bytes(const mlra_dims* d, int width) { return (size_t)d->num_pages * kPage * width * dtype_bytes(d); }
+size_t table_bytes(const mlra_dims* d) { return (size_t)d->B * d->max_pages_per_seq * 4; }
+
 // ---------------------------------------------------------------------------
 // prompt
 // ---------------------------------------------------------------------------
@@ -158,6 +179,11 @@ size_t prompt_workspace(const mlra_dims* d, const PromptArgs& a) {
                                                                                                  : kErrBytes;
 }
 
+// Bytes from the first element of a packed array to behind its last.
+size_t packed_bytes(const mlra_dims* d, int rows, int heads, int width, const long long* s) {
+  return rows == 0 ? 0 : ((size_t)(rows - 1) * s[0] + (size_t)(heads - 1) * s[1] + width) * dtype_bytes(d);
+}
+
 // Copies by the tensor memory accelerator: 16-byte addresses and strides.
 bool prompt_aligned(const PromptArgs& a, const void* q_nope, const void* q_rope, const void* k_nope, const void* v) {
   const void* p[] = {q_nope, q_rope, k_nope, v};
@@ -196,7 +222,7 @@ mlra_status mla_prompt(const mlra_dims* dims, const mla_prompt_shape* shape, con
     if (st != MLRA_OK) return st;
     const mlra_dims* d = dims;
     const mla_prompt_shape* s = shape;
-    const size_t e = d->dtype == MLRA_BF16 ? 2 : 4;
+    const size_t e = dtype_bytes(d);
     const Named ptrs[] = {{cu_q, "cu_q", 4},     {cu_k, "cu_k", 4}, {rope_cache, "rope_cache", 16},
                           {page_table, "page_table", 4}, {q_nope, "q_nope", e}, {q_rope, "q_rope", e},
                           {out, "out", 16},      {k_nope, "k_nope", e}, {v, "v", e}};
@@ -218,6 +244,18 @@ mlra_status mla_prompt(const mlra_dims* dims, const mla_prompt_shape* shape, con
                  "the tcgen05 prompt kernel needs bf16, d_h=128, d_r=64, d_v=128 and 16-byte aligned rows");
     if (path == PromptPath::kNoRegisters)
       return bad(MLRA_ERR_UNSUPPORTED, "the tcgen05 prompt kernel was compiled to %d registers, not %d", regs, want);
+    const size_t cu = (size_t)(d->B + 1) * 4, rows = (size_t)s->total_q * d->H;
+    const Span in[] = {{q_nope, packed_bytes(d, s->total_q, d->H, d->d_h, s->q_nope_stride)},
+                       {q_rope, packed_bytes(d, s->total_q, d->H, d->d_r, s->q_rope_stride)},
+                       {k_nope, packed_bytes(d, s->total_k, s->kv_heads, d->d_h, s->k_nope_stride)},
+                       {v, packed_bytes(d, s->total_k, s->kv_heads, d->d_v, s->v_stride)},
+                       {cu_q, cu},
+                       {cu_k, cu},
+                       {rope_cache, pool_bytes(d, d->d_r)},
+                       {page_table, table_bytes(d)}},
+               outs[] = {{out, rows * d->d_v * e}, {lse, rows * 4}, {workspace, prompt_workspace(d, a)}};
+    st = check_overlap(in, outs);
+    if (st != MLRA_OK) return st;
     const RopeTable tab = internal_rope_table(d);
     if (path == PromptPath::kTc) {
       const int sms = device_sms();
@@ -248,6 +286,14 @@ mlra_status mlra_absorb(const mlra_dims* dims, const void* q_nope, const void* q
     const bool tc_ok = absorb_tc_supported(d->dtype, d->B, d->d_h, d->d_c) && d->d_r % 8 == 0;
     if (d->kernel == MLRA_KERNEL_TC && !tc_ok)
       return bad(MLRA_ERR_UNSUPPORTED, "the tcgen05 absorption does not take this shape");
+    const size_t e = dtype_bytes(d), rows = (size_t)d->B * d->H;
+    const Span in[] = {{q_nope, rows * d->d_h * e},
+                       {q_rope, rows * d->d_r * e},
+                       {q_pos, (size_t)d->B * 4},
+                       {W_UK, (size_t)d->H * d->d_h * d->d_c * e}},
+               outs[] = {{q_abs, rows * (d->d_c + d->d_r) * e}, {workspace, kErrBytes}};
+    st = check_overlap(in, outs);
+    if (st != MLRA_OK) return st;
     const RopeTable tab = internal_rope_table(d);
     const float q_scale = scale_log2(d);
     if (tc_ok && d->kernel != MLRA_KERNEL_SIMT) {
@@ -281,7 +327,7 @@ mlra_status mlra_attention_weights(const mlra_dims* dims, const void* q_abs, con
     st = check_ptrs(ptrs, 7);
     if (st == MLRA_OK && weights_in && !aligned(weights_in, 4))
       st = bad(MLRA_ERR_INVALID_ARG, "weights_in is not 4-byte aligned");
-    const size_t bytes = (size_t)d->B * d->max_pages_per_seq * kPage * 4;
+    const size_t bytes = table_bytes(d) * kPage;
     if (st == MLRA_OK && weights_in && weights_in != weights && overlap(weights_in, bytes, weights, bytes))
       st = bad(MLRA_ERR_INVALID_ARG, "weights_in and weights overlap in part");
     if (st == MLRA_OK) st = check_workspace(workspace, workspace_bytes, kErrBytes);
@@ -291,6 +337,17 @@ mlra_status mlra_attention_weights(const mlra_dims* dims, const void* q_abs, con
       return bad(MLRA_ERR_UNSUPPORTED,
                  "the tcgen05 weights kernel needs bf16, d_r=64, branches of a multiple of 64 dims, H<=128 and "
                  "n_branch * H (in steps of 32) <= 512");
+    const Span in[] = {{q_abs, (size_t)d->B * d->H * (d->d_c + d->d_r) * dtype_bytes(d)},
+                       {lse, (size_t)d->B * d->n_branch * d->H * 4},
+                       {latent_cache, pool_bytes(d, d->d_c)},
+                       {rope_cache, pool_bytes(d, d->d_r)},
+                       {page_table, table_bytes(d)},
+                       {seq_lens, (size_t)d->B * 4}},
+               outs[] = {{weights, bytes}, {workspace, kErrBytes}};
+    st = check_overlap(in, outs);
+    if (st == MLRA_OK && weights_in && overlap(weights_in, bytes, workspace, kErrBytes))
+      st = bad(MLRA_ERR_INVALID_ARG, "an output overlaps an input");
+    if (st != MLRA_OK) return st;
     const int sms = device_sms();
     if (sms == 0) return MLRA_ERR_CUDA;
     const WeightArgs a{d->B, d->H, d->d_c, d->d_r, d->n_branch, d->max_pages_per_seq, d->num_pages};
@@ -363,25 +420,19 @@ mlra_status latent_evict(const mlra_dims* dims, int recent, const int32_t* evict
                           {seq_lens_out, "seq_lens_out", 4}};
     st = check_ptrs(ptrs, 9);
     if (st != MLRA_OK) return st;
-    const size_t row = (size_t)d->B * d->max_pages_per_seq * 4, e = d->dtype == MLRA_BF16 ? 2 : 4;
-    const struct {
-      const void* p;
-      size_t n;
-    } in[] = {{evict_pages, (size_t)d->B * 4}, {weights, row * kPage}, {page_table, row}, {seq_lens, (size_t)d->B * 4}},
-      outs[] = {{weights_out, row * kPage},
-                {page_table_out, row},
-                {seq_lens_out, (size_t)d->B * 4},
-                {latent_cache, (size_t)d->num_pages * kPage * d->d_c * e},
-                {rope_cache, (size_t)d->num_pages * kPage * d->d_r * e}};
-    for (int o = 0; o < 5; ++o) {
-      for (const auto& i : in)
-        if (overlap(i.p, i.n, outs[o].p, outs[o].n)) return bad(MLRA_ERR_INVALID_ARG, "an output overlaps an input");
-      for (int q = 0; q < o; ++q)
-        if (overlap(outs[q].p, outs[q].n, outs[o].p, outs[o].n))
-          return bad(MLRA_ERR_INVALID_ARG, "two outputs overlap");
-    }
     const EvictLayout l = evict_layout(d);
     st = check_workspace(workspace, workspace_bytes, l.total);
+    if (st != MLRA_OK) return st;
+    const size_t row = table_bytes(d), e = dtype_bytes(d);
+    const Span in[] = {{evict_pages, (size_t)d->B * 4}, {weights, row * kPage}, {page_table, row},
+                       {seq_lens, (size_t)d->B * 4}},
+               outs[] = {{weights_out, row * kPage},
+                         {page_table_out, row},
+                         {seq_lens_out, (size_t)d->B * 4},
+                         {latent_cache, pool_bytes(d, d->d_c)},
+                         {rope_cache, pool_bytes(d, d->d_r)},
+                         {workspace, l.total}};
+    st = check_overlap(in, outs);
     if (st != MLRA_OK) return st;
     const int sms = device_sms();
     if (sms == 0) return MLRA_ERR_CUDA;
