@@ -50,7 +50,9 @@ __global__ void __launch_bounds__(kPThreads * kG)
   float* sp = sv + kPk * vp;                                 // [kPq][kPk + 1], at the end its maxima and sums
   auto group_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(kPThreads) : "memory"); };
   __shared__ int s_b, s_tile;
-  // tile blockIdx.x of the batch: the tiles of the sequences one after another
+  // Tile blockIdx.x of the batch: the tiles of the sequences one after another.  The grid has room for sequences that
+  // do not overlap; overlapping ones have a descending pair of offsets between them, which the last CTA walks past
+  // and reports.
   if (threadIdx.x == 0) {
     int t = blockIdx.x, b = 0;
     for (; b < a.B; ++b) {
@@ -58,11 +60,6 @@ __global__ void __launch_bounds__(kPThreads * kG)
       const int n = (s.Lq + kPq - 1) / kPq;
       if (t < n) break;
       t -= n;
-    }
-    // the grid has a tile more than sequences that do not overlap can have
-    if (blockIdx.x == gridDim.x - 1 && b < a.B) {
-      report_error(err, kErrDeviceCheck, a.B, a.total_q);
-      b = a.B;
     }
     s_b = b;
     s_tile = t;

@@ -127,3 +127,29 @@ def test_prompt_keys_of_later_tokens_do_not_reach_a_query(dtype):
     for rows in (slice(0, 170), slice(200, 264)):
         assert torch.equal(_bits(p.out[rows]), _bits(want[rows])) and torch.equal(p.lse[rows], want_lse[rows])
     assert p.out[170:200].isnan().all() and p.out[284:290].isnan().all()
+
+
+# ---------------------------------------------------------------------------
+# sequences that overlap
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_overlapping_sequences_stay_in_the_workspace(dtype):
+    """41 times the same rows, with a descending pair of offsets between them: more tiles than the lists have room for."""
+    T, B = 1024, 81
+    p = _prompt(dtype, (T,) + (0,) * (B - 1), (T,) + (0,) * (B - 1), 2, 2, seed=23)
+    assert (B + 1) // 2 * T // 256 > (p.out.shape[0] + 255) // 256 + B
+    for cu in (p.cu_q, p.cu_k):
+        cu[:] = torch.tensor([T * (i % 2) for i in range(B + 1)], dtype=torch.int32)
+    p.table[:] = p.table[:1].clone()
+    size, guard = p.ws.numel(), 1 << 16
+    whole = torch.full((size + guard,), 0x5a, dtype=torch.uint8, device="cuda")
+    whole[:256] = 0
+    p.ws = whole[:size]
+    p.call()
+    with pytest.raises(abi.MlraError):
+        abi.check_status(p.ws)
+    assert (whole[size:] == 0x5a).all()
+    assert p.out[T:].isnan().all() and p.lse[T:].isnan().all()
+    if dtype == "bf16":  # the plan is not made: no row is written, and no item listed
+        assert p.out.isnan().all() and p.lse.isnan().all()
+        assert (whole[512:512 + 8 * (T // 256 + B)] == 0x5a).all()
