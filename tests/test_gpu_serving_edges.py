@@ -153,3 +153,26 @@ def test_prompt_overlapping_sequences_stay_in_the_workspace(dtype):
     if dtype == "bf16":  # the plan is not made: no row is written, and no item listed
         assert p.out.isnan().all() and p.lse.isnan().all()
         assert (whole[512:512 + 8 * (T // 256 + B)] == 0x5a).all()
+
+
+# ---------------------------------------------------------------------------
+# peaked scores
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,kernel", [("f32", "auto"), ("bf16", "auto"), ("bf16", "simt")])
+def test_prompt_peaked_scores(dtype, kernel):
+    """Scores of a standard deviation of 24 (fp32: 49) without a rotary part, whose rounding would be most of the bound:
+    the running maximum jumps by far more than the kernel puts up with, and the bound stays near the output's rounding."""
+    p = _prompt(dtype, (150, 300), (150, 700), 4, 4, scale=30.0 if dtype == "bf16" else 60.0, seed=24, kernel=kernel)
+    p.q_rope[:] = 0
+    p.call()
+    assert _check(p) < 0.05
+
+
+def test_prompt_scores_that_rise():
+    """By 0.14 a key: the maximum moves by 18 in every step of 128 keys, and only a row's last keys count."""
+    p = _prompt("bf16", (500,), (900,), 2, 1, scale=0.1, seed=25)
+    p.q_rope[:] = 0
+    p.q_nope[:, :, 0] = 1.0
+    p.k_nope[:900, :, 0] = (2.0 * torch.arange(900, device="cuda")).to(torch.bfloat16)[:, None]
+    p.call()
+    assert _check(p) < 0.05
