@@ -176,3 +176,95 @@ def test_prompt_scores_that_rise():
     p.k_nope[:900, :, 0] = (2.0 * torch.arange(900, device="cuda")).to(torch.bfloat16)[:, None]
     p.call()
     assert _check(p) < 0.05
+
+
+# ---------------------------------------------------------------------------
+# more work items than CTAs
+# ---------------------------------------------------------------------------
+def _items(p):
+    """Pairs of 128-row tiles of the tcgen05 kernel."""
+    group = p.H // p.kv
+    pack = min(128, group & -group)
+    pairs = sum(-(-int(n) * pack // 256) for n in p.cu_q[1:] - p.cu_q[:-1])
+    return pairs * (p.H // pack)
+
+
+def _twice(p):
+    p.call()
+    out, lse = p.out.clone(), p.lse.clone()
+    p.out.fill_(float("nan"))
+    p.lse.fill_(float("nan"))
+    p.call()
+    assert torch.equal(_bits(out), _bits(p.out)) and torch.equal(_bits(lse), _bits(p.lse))
+
+
+# single tokens, key lengths around the tiles' ends, contexts, more queries than keys (whose first tiles have no key),
+# sequences without queries or keys: what one item leaves behind meets every kind of next one
+MIXED_Q = (1, 700, 64, 257, 129, 5, 0, 300, 128, 3, 513, 40, 256, 90, 1, 640)
+MIXED_K = (1, 700, 500, 257, 130, 900, 70, 10, 128, 0, 800, 1300, 255, 91, 2000, 300)
+
+
+@pytest.mark.parametrize("H,kv", [(32, 32), (48, 16), (96, 48)])
+def test_prompt_several_items_a_cta(H, kv):
+    p = _prompt("bf16", MIXED_Q, MIXED_K, H, kv, seed=26)
+    assert _items(p) > 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    _twice(p)
+    _check(p)
+
+
+def test_prompt_several_items_a_cta_of_packed_heads():
+    p = _prompt("bf16", MIXED_Q * 3, MIXED_K * 3, 64, 4, seed=27)
+    assert _items(p) > 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    _twice(p)
+    _check(p, heads=(0, 17, 38, 63))
+
+
+def test_prompt_many_items_with_values_that_are_not_finite():
+    """Items to be taken again between others that are not, several of a CTA."""
+    H, kv = 48, 24
+    p = _prompt("bf16", MIXED_Q * 2, MIXED_K * 2, H, kv, seed=28)
+    clean, hit = p.v.clone(), torch.zeros_like(p.out, dtype=torch.bool)
+    for b in range(0, len(MIXED_Q) * 2, 3):
+        q0, q1, k0, k1 = (int(cu[b + i]) for cu in (p.cu_q, p.cu_k) for i in (0, 1))
+        for n, g in enumerate(range(b % 2, kv, 2)):
+            j = (k1 - k0) * (n + 1) // kv  # the keys of a prompt's first half and more
+            if j < k1 - k0:
+                p.v[k0 + j, g, b] = float("inf")
+                hit[q0 + max(0, j - (k1 - k0 - (q1 - q0))):q1, 2 * g:2 * g + 2, b] = True
+    _twice(p)
+    _check(p, v=clean, skip=hit)
+    assert p.out[hit].isposinf().all()
+
+
+@pytest.mark.parametrize("H,kv", [(128, 128), (128, 64)])
+def test_prompt_groups_of_heads(H, kv):
+    """More K and V than L2 holds: the heads are taken in groups, the last of them smaller (128 kv heads: 43 + 43 + 42)."""
+    p = _prompt("bf16", (300, 2), (4100, 200), H, kv, seed=29)
+    units = H // (H // kv)
+    group = (112 << 20) // (p.k_nope.shape[0] * 512 * kv // units)
+    groups = -(-units // group)
+    assert groups > 1 and (kv < 128 or units % groups)
+    assert _items(p) > torch.cuda.get_device_properties(0).multi_processor_count
+    _twice(p)
+    _check(p, heads=(0, 1, 41, 42, 43, 44, 85, 86, 87, 126, 127))
+
+
+def test_prompt_two_calls_at_once():
+    """Two batches on two streams, a workspace each: the same bits as one after the other."""
+    a, b = (_prompt("bf16", MIXED_Q, MIXED_K, 24, 24, seed=30 + i) for i in range(2))
+    a.call()
+    b.call()
+    want = [x.clone() for x in (a.out, b.out, a.lse, b.lse)]
+    for x in (a, b):
+        x.out.fill_(float("nan"))
+        x.lse.fill_(float("nan"))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for p, s in zip((a, b), streams):
+            p.call(stream=s)
+    torch.cuda.synchronize()
+    for x, y in zip(want, (a.out, b.out, a.lse, b.lse)):
+        assert torch.equal(_bits(x), _bits(y))
+    abi.check_status(a.ws)
+    abi.check_status(b.ws)
