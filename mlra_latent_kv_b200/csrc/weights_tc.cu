@@ -10,8 +10,9 @@
 // branches of 128 heads: 149 to 161 us under the power cap, 125 in a burst.
 //
 // The tensor core's fp32 sums truncate: a logit is a few units in its last
-// place low in magnitude, a weight within 4e-6.  The log-sum-exp of the decode
-// kernels comes from sums of the same kind.
+// place low in magnitude.  All weights together are 1e-6 to 2e-6 from the 64-bit
+// ones (2-norm), a single one up to 1.2e-5 of itself.  The log-sum-exp of the
+// decode kernels comes from sums of the same kind.
 //
 // Design (B200):
 //   * The tokens are the rows of the product: S^T[128 tokens, heads] =
@@ -22,8 +23,8 @@
 //     128 rows is spent on tokens, of which there are plenty, not on heads.
 //   * The query of the current sequence stays in shared memory (147 KB at 128
 //     heads), the cache passes through two rings of 16 KB blocks (128 tokens x
-//     64 dims), latent and rotary, that fill the rest: 80 KB in flight at 128
-//     heads, 176 KB at 32.
+//     64 dims), latent and rotary, that fill the rest: 64 KB in flight at 128
+//     heads, 176 KB at 32 (ring_blocks).
 //   * A unit is (tile, branch), its scores one of 512 / heads TMEM buffers.  The
 //     tile's rotary block starts each branch's buffer when its turn comes and
 //     stays (loaded once) until the last branch's, the branch's latent blocks
@@ -74,6 +75,14 @@ struct WtBars {
 };
 
 static_assert(offsetof(WtBars, lse) % 16 == 0 && sizeof(WtBars) % 16 == 0, "16-byte reads");
+
+// 16 KB blocks of both rings beside the query of Hp heads and D dims: a block is missing at 128 heads, where the
+// barriers and the log-sum-exps take what is left of it.
+constexpr int query_bytes(int Hp, int D) { return D / 64 * Hp * 128; }
+constexpr int ring_blocks(int Hp, int D) {
+  return (kWtSmem - 1024 - query_bytes(Hp, D) - (int)sizeof(WtBars)) / kWtBlock;
+}
+static_assert(ring_blocks(128, 576) == 4 && ring_blocks(32, 576) == 11, "64 KB and 176 KB");
 
 // A position in a ring of `n` barriers and the parity of its current round.
 struct RingPos {
@@ -414,10 +423,9 @@ cudaError_t launch_weights_tc(const void* q_abs, const float* lse, const void* l
         !encode_bf16_map(&tq, 3, q_abs, qd, qs, qbox))
       return cudaErrorInvalidValue;
   }
-  const int q_bytes = (D / 64) * Hp * 128;
-  const int fit = (kWtSmem - 1024 - q_bytes - (int)sizeof(WtBars)) / kWtBlock;
+  const int q_bytes = query_bytes(Hp, D), fit = ring_blocks(Hp, D);
   if (fit < 3) return cudaErrorInvalidValue;
-  // a second rotary block where there is room (128 heads: four latent blocks and one)
+  // a second rotary block where there is room (128 heads: three latent blocks and one)
   const int ropes = fit < 6 ? 1 : kWtRopes, stages = fit - ropes < kWtStages ? fit - ropes : kWtStages;
   const int stride = (Hp + 31) / 32 * 32;
   const int bufs = 512 / stride < kWtBufs ? 512 / stride : kWtBufs;
