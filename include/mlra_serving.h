@@ -148,7 +148,8 @@ MLRA_SERVING_API mlra_status mlra_attention_weights(const mlra_dims* dims, const
  *     in their new slots, zeros behind them
  *   page_table_out [B, max_pages_per_seq]: the row without its first n
  *     entries, -1 behind it; entries [0, n) of the old row are the pages that
- *     are free now
+ *     this sequence no longer names (a prefix that it shares with others lies
+ *     among them: such a page is free only when no sequence names it)
  *   seq_lens_out [B] = seq_lens[b] - 64 n
  * Decode with page_table_out and seq_lens_out.  Positions do not change: q_pos stays the token's position,
  * and latent_append, which finds a token's slot by its position, keeps taking

@@ -409,8 +409,8 @@ def evict_workspace_bytes(dims: Dims) -> int:
 
 def latent_evict(dims, recent, evict_pages, weights, page_table, seq_lens, latent_cache, rope_cache, weights_out,
                  page_table_out, seq_lens_out, workspace, stream=None):
-    """Frees evict_pages[b] pages of each sequence: the tokens with the least weight leave, but for the last
-    ``recent`` (see include/mlra_serving.h)."""
+    """Takes evict_pages[b] pages from each sequence: the tokens with the least weight leave, but for the last
+    ``recent`` (see include/mlra_serving.h; a page that another sequence shares is not free then)."""
     recent = _int32("recent", recent)
     B, pages = dims.B, dims.max_pages_per_seq
     ty, pool = _types(), (dims.num_pages, dims.page_size)
