@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from mlra_latent_kv_b200 import abi
-from test_gpu_serving import FULL, TINY, TORCH, U16, U32, Prompt
+from test_gpu_serving import FULL, TINY, U16, U32, Evict, Prompt, Weights
 
 pytestmark = pytest.mark.gpu
 
@@ -268,3 +268,35 @@ def test_prompt_two_calls_at_once():
         assert torch.equal(_bits(x), _bits(y))
     abi.check_status(a.ws)
     abi.check_status(b.ws)
+
+
+# ---------------------------------------------------------------------------
+# eviction and weights
+# ---------------------------------------------------------------------------
+def test_evict_of_a_shared_prefix_reads_it_for_each_sequence():
+    """Three sequences begin with the same four pages; two of them give exactly these up, the third keeps them."""
+    x = Evict("bf16", (1000, 700, 500), (4, 4, 0), 20, seed=40)
+    x.table[1:, :4] = x.table[:1, :4].clone()
+    x.lat.nan_to_num_(0.5), x.rope.nan_to_num_(0.5)  # the pages that nobody names any more
+    want = x.expected()
+    prefix = x.table[0, :4].long()
+    before = x.lat[prefix].clone()
+    x.call()
+    x.check(want)
+    assert torch.equal(_bits(x.lat[prefix]), _bits(before))
+
+
+def test_weights_and_evict_on_another_stream():
+    w, e = Weights("bf16", (3000, 77), 32, 1, FULL, seed=41), Evict("bf16", (900, 2000), (6, 20), 64, seed=42)
+    want = e.expected()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    w.call(stream=side)
+    e.call(stream=side)
+    with torch.cuda.stream(side):  # and on the stream that is current
+        e.call()
+        w.call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    w.check()
+    e.check(want)
