@@ -47,7 +47,7 @@
 //     to 923 TFLOP/s at the 1545 MHz that the power cap leaves, 640 in a burst;
 //     16 ragged sequences up to 1900 tokens, 32 heads 146 us; four chunks behind
 //     up to 8000 tokens, 32 heads on 8, 264 us.  The tensor pipe is active 55 %.
-//   * Registers: 168 a thread with 88 bytes of spill stores and 440 of loads
+//   * Registers: 168 a thread with 88 bytes of spill stores and 456 of loads
 //     (-Xptxas -v).  Compiled to 116 and 132 the same work takes 3 % longer.
 //   * Every wait is bounded; a CTA that gives up records the site, lets its
 //     copies and MMAs in flight end and leaves.
@@ -244,11 +244,11 @@ __global__ void __launch_bounds__(kPlanThreads)
 // lane per key for the scores, four columns a lane for the values.
 //
 // Taken in turns with the kernel that did not look, 128 heads x 4096 tokens
-// 708-744 -> 717-751 us, the ragged batch 131-136 -> 133-140, grouped chunks
-// 247-250 -> 249-254.  (In the epilogue of the softmax warps it cost 3 to 8 %, for
-// the compiler then spilled in their loop; in a kernel of its own behind this one
-// the second part took 2 to 3 us.)  Rows are taken again in short loops that are
-// not unrolled: one token of NaN in all of 128 heads x 4096 tokens takes 51 ms.
+// 736-747 -> 738-742 us, the ragged batch 135-137 -> 138-140, grouped chunks
+// 246 -> 250.  (In the epilogue of the softmax warps it cost 3 to 8 %, for the
+// compiler then spilled in their loop; in a kernel of its own behind this one the
+// second part took 2 to 3 us.)  One token of NaN in all of 128 heads x 4096 tokens
+// takes 20 ms: 24 reads of a key and eight values at a time, each from L2.
 // ---------------------------------------------------------------------------
 struct PromptRows {
   const __nv_bfloat16 *q_nope, *q_rot, *k_nope, *v, *rope_cache;
@@ -342,9 +342,9 @@ __device__ __forceinline__ void rows_again(const PromptItem& it, int first, cons
         if (id < 0 || id >= a.num_pages) id = 0;  // reported when its step was loaded
         const uint4* kr = reinterpret_cast<const uint4*>(rows.rope_cache + ((size_t)id * kPage + j % kPage) * 64);
         float s = 0.f;
-#pragma unroll 1
+#pragma unroll 4
         for (int c = 0; c < 16; ++c) s = dot8(__ldg(qn + c), __ldg(kn + c), s);
-#pragma unroll 1
+#pragma unroll 4
         for (int c = 0; c < 8; ++c) s = dot8(qr[c], __ldg(kr + c), s);
         s = j0 + lane <= lim ? s * a.scale_log2 : -INFINITY;
         float top = s;
@@ -357,14 +357,18 @@ __device__ __forceinline__ void rows_again(const PromptItem& it, int first, cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] *= corr;
 #pragma unroll 1
-        for (int u = 0; u < 32; ++u) {
-          if (j0 + u > lim) break;
-          const float pu = __shfl_sync(0xffffffffu, p, u);
-          const uint2 y = value(j0 + u);
-          o[0] = fmaf(pu, __uint_as_float(y.x << 16), o[0]);
-          o[1] = fmaf(pu, __uint_as_float(y.x & 0xffff0000u), o[1]);
-          o[2] = fmaf(pu, __uint_as_float(y.y << 16), o[2]);
-          o[3] = fmaf(pu, __uint_as_float(y.y & 0xffff0000u), o[3]);
+        for (int u0 = 0; u0 < 32 && j0 + u0 <= lim; u0 += 8) {
+          uint2 y[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) y[u] = j0 + u0 + u <= lim ? value(j0 + u0 + u) : make_uint2(0u, 0u);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float pu = __shfl_sync(0xffffffffu, p, u0 + u);
+            o[0] = fmaf(pu, __uint_as_float(y[u].x << 16), o[0]);
+            o[1] = fmaf(pu, __uint_as_float(y[u].x & 0xffff0000u), o[1]);
+            o[2] = fmaf(pu, __uint_as_float(y[u].y << 16), o[2]);
+            o[3] = fmaf(pu, __uint_as_float(y[u].y & 0xffff0000u), o[3]);
+          }
         }
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
