@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 // Taken in turns with the kernel that did not look, 128 heads x 4096 tokens
 // 736-747 -> 738-742 us, the ragged batch 135-137 -> 138-140, grouped chunks
 // 246 -> 250.  (In the epilogue of the softmax warps it cost 3 to 8 %, for the
-// compiler then spilled in their loop; in a kernel of its own behind this one the
-// second part took 2 to 3 us.)  One token of NaN in all of 128 heads x 4096 tokens
+// compiler then dealt their loop's registers otherwise; in a kernel of its own
+// behind this one the second part took 2 to 3 us.)  One token of NaN in all of 128 heads x 4096 tokens
 // takes 20 ms: 24 reads of a key and eight values at a time, each from L2.
 // ---------------------------------------------------------------------------
 struct PromptRows {
